@@ -361,6 +361,102 @@ RAG_API rag_status rag_recompute_kv(const rag_kv_pool* pool, int32_t layer, cons
  * RAG_ERR_GEOMETRY. */
 RAG_API rag_status rag_recompute_status(const void* plan, int32_t* counts, void* stream);
 
+/* ---- Growing caches: new tokens appended to paged sequences --------------------
+ * The generation continues on the concatenated cache (TurboRAG page,
+ * "Technical Details", listing `turborag_inference`), with one set of position
+ * ids for precompute and inference (its "Implementation"): the K, V of a
+ * request's prompt and of every token it generates join the request's own
+ * pages, K carrying the rotation of its position. A pool is held in 16 bits
+ * (rag_kv_pool) or in 8 (rag_kv8_pool). */
+
+/* The tokens one call appends to n_seqs sequences. The int32 arrays are DEVICE
+ * pointers. Sequence s takes rows tok_off[s] .. tok_off[s+1]-1 of k, v and q as
+ * its tokens start[s], start[s]+1, ...; its token i lives in slot i % 16 of page
+ * page_ids[page_off[s] + i / 16] and has rotary position pos0[s] + i.
+ *   tok_off  [n_seqs+1]   prefix over sequences of new tokens (0 is allowed)
+ *   start    [n_seqs]     tokens the sequence holds already
+ *   page_off [n_seqs+1]   prefix over sequences of pages; they must hold
+ *                         start[s] + new tokens
+ *   page_ids [total_pages]
+ *   pos0     [n_seqs]     optional (NULL: 0): position of the sequence's token 0
+ * total_new and total_pages bound the prefixes; rows of k, v, q from
+ * tok_off[n_seqs] to total_new-1 are padding: not read, and their rows of q_out
+ * are left as they were. A page that receives tokens belongs to one sequence of
+ * the call. With fixed arrays whose contents the caller advances on the device,
+ * a captured call can be replayed. */
+typedef struct {
+  int32_t n_seqs;      /* 0 .. 65536 */
+  int32_t total_new;
+  int32_t total_pages;
+  const int32_t* tok_off;
+  const int32_t* start;
+  const int32_t* page_off;
+  const int32_t* page_ids;
+  const int32_t* pos0;
+} rag_append;
+
+/* Table of rotations: table[p * head_dim/2 + j] = (cos, sin) of the angle
+ * p * base^(-2j/head_dim), p = 0 .. n_pos-1 (fp32 pairs, computed in fp64).
+ * Built once, read by every append. base > 1, head_dim 64 or 128. */
+RAG_API rag_status rag_rope_cos_sin(double base, int32_t head_dim, int32_t n_pos, float* table, void* stream);
+
+/* Append to a 16-bit (or fp32) pool.
+ * k, v  [total_new] rows of num_kv_heads * head_dim values, pool dtype (bf16 or
+ *       fp32), rows k_stride and v_stride ELEMENTS apart (slices of one fused
+ *       projection are fine); row pointers and strides 16-byte aligned
+ * rope  [n_pos][head_dim/2] (cos, sin), 16-byte aligned, or NULL: K as it is.
+ *       The pair (j, j + head_dim/2) is turned as a c - b s, b c + a s, every
+ *       product and sum rounded to fp32, the result once to the stored type;
+ *       V is stored like rag_kv_pool_write's (a bf16 pool keeps fp16)
+ * q     optional: [total_new] rows of num_q_heads * head_dim values, q_stride
+ *       elements apart, rotated the same way into the dense
+ *       q_out [total_new][num_q_heads][head_dim] (may be q itself when dense)
+ * When the call writes slot 0 of a page, the page's slots behind the call's
+ * last token are zeroed; other slots keep what they hold.
+ * *device_err (optional device int32) collects bits: 1 a page id outside the
+ * pool (its tokens are not stored), 2 a sequence whose descriptors are
+ * inconsistent (not stored; q_out rows zero) or a position outside [0, n_pos)
+ * (that token is stored as zeros; its q_out row is zero), 8 a V value
+ * saturated. */
+RAG_API rag_status rag_kv_append(const rag_kv_pool* pool, int32_t layer, const rag_append* seqs, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, const float* rope, int32_t n_pos,
+                                 const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                                 int32_t* device_err, void* stream);
+
+/* The pool held in 8 bits (caller-owned device memory).
+ * k, v             [num_layers][num_pages][num_kv_heads][16][128] e4m3 codes
+ * k_scale, v_scale [num_layers][num_pages][num_kv_heads] fp32
+ * value = code * scale of its page and head. rag_kv8_append keeps the scales
+ * powers of two, at least 2^-24. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_layers;
+  int32_t num_pages;
+  int32_t num_kv_heads;
+  int32_t page_size; /* must be RAG_PAGE_SIZE */
+  int32_t head_dim;  /* must be 128 */
+} rag_kv8_pool;
+
+/* Append to an 8-bit pool; arguments as rag_kv_append's, k, v, q in bf16. Per
+ * (page, head) and tensor: need = the smallest power of two, at least 2^-24
+ * (and at most 2^7 for V), with the largest new magnitude <= 448 * need; the
+ * page's scale becomes need when the call writes its slot 0, else the larger
+ * of need and the scale it has. New codes are e4m3(value / scale), rounded to
+ * nearest even. Where the scale grows, the held codes become
+ * e4m3(code * old / new): exact but for values that fall below e4m3's normal
+ * range, since the ratio is a power of two. Chunks are written by appending
+ * their tokens to an empty sequence.
+ * inf saturates, nan is stored as 0, and V saturates beyond 57,344: all three
+ * raise bit 8 (RAG_ERR_RANGE) of *device_err; the other bits are
+ * rag_kv_append's. */
+RAG_API rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_append* seqs, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, const float* rope,
+                                  int32_t n_pos, const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                                  int32_t* device_err, void* stream);
+
 /* Synchronise `stream`, read and clear the workspace error word. Returns
  * RAG_OK when the device reported nothing, else the most severe of
  * RAG_ERR_TIMEOUT, RAG_ERR_PAGE_OOB, RAG_ERR_GEOMETRY, RAG_ERR_RANGE; *bits
@@ -392,7 +488,8 @@ RAG_API int64_t rag_launch_count(void);
  * 2 split combine, 3 impact, 4 top-k, 5 fp32 attention, 6 fp32 impact,
  * 7 recompute plan, 8 recompute page copy, 9 recompute projection,
  * 10 RoPE table, 11 KV decode, 12 attention of query blocks of at most 16
- * rows, e.g. decode steps) into
+ * rows, e.g. decode steps, 13 append, 14 8-bit append, 15 table of rotations)
+ * into
  * the first n_kinds entries of ms and launches (either may be NULL), and
  * resets the record. */
 RAG_API void rag_profile_enable(int32_t on);

@@ -7,7 +7,9 @@ is its thin ctypes binding.
 """
 
 from .rag import (  # noqa: F401
+    Append,
     Batch,
+    KV8Pool,
     KVPool,
     RagError,
     lib,
@@ -16,6 +18,8 @@ from .rag import (  # noqa: F401
     rag_fused_prefill_attn,
     rag_fused_prefill_attn_rope,
     rag_impact_topk,
+    rag_kv8_append,
+    rag_kv_append,
     rag_kv_decode,
     rag_kv_pool_write,
     rag_last_device_error,
@@ -29,6 +33,7 @@ from .rag import (  # noqa: F401
     rag_recompute_plan,
     rag_recompute_plan_size,
     rag_recompute_status,
+    rag_rope_cos_sin,
     rag_workspace_size,
     topk_capacity,
 )

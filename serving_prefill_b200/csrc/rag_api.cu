@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "rag_prefill.h"
+#include "host.cuh"
 #include "params.cuh"
 
 namespace rag {
@@ -23,9 +24,6 @@ constexpr int kTopkMaxKHost = 16384;
 constexpr int kRcMinDModel = 64;
 
 // ------------------------------------------------------------ profiling
-
-enum Kind { kKindPoolWrite = 0, kKindAttn, kKindCombine, kKindImpact, kKindTopk, kKindSimtAttn, kKindSimtImpact,
-            kKindRcPlan, kKindRcCopy, kKindRcGemm, kKindRope, kKindKvDecode, kKindDecAttn, kNumKinds };
 
 struct ProfRecord {
   int kind;
@@ -64,28 +62,24 @@ static void record_event(cudaEvent_t ev, cudaStream_t stream) {
     cudaEventRecord(ev, stream);
 }
 
-struct LaunchScope {
-  int kind;
-  cudaStream_t stream;
-  cudaEvent_t start = nullptr, stop = nullptr;
-  LaunchScope(int k, cudaStream_t s) : kind(k), stream(s) {
-    if (g_prof_on.load()) {
-      std::lock_guard<std::mutex> lk(g_prof_mu);
-      start = take_event();
-      stop = take_event();
-      record_event(start, stream);
-    }
+LaunchScope::LaunchScope(int k, cudaStream_t s) : kind(k), stream(s) {
+  if (g_prof_on.load()) {
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    start = take_event();
+    stop = take_event();
+    record_event(start, stream);
   }
-  void done(cudaError_t e) {
-    if (e == cudaSuccess) g_launches.fetch_add(1);
-    else note_cuda_error(e);
-    if (start) {
-      record_event(stop, stream);
-      std::lock_guard<std::mutex> lk(g_prof_mu);
-      g_prof.push_back({kind, start, stop});
-    }
+}
+
+void LaunchScope::done(cudaError_t e) {
+  if (e == cudaSuccess) g_launches.fetch_add(1);
+  else note_cuda_error(e);
+  if (start) {
+    record_event(stop, stream);
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    g_prof.push_back({kind, start, stop});
   }
-};
+}
 
 // ------------------------------------------------------------ tensor maps
 
@@ -112,6 +106,7 @@ struct MapKey {
   uint64_t dims[3];
   uint64_t strides[2];
   uint32_t box[3];
+  uint32_t bytes;   // 1: 8-bit elements, 0: bf16
   bool operator==(const MapKey& o) const { return std::memcmp(this, &o, sizeof(MapKey)) == 0; }
 };
 struct MapKeyHash {
@@ -124,13 +119,13 @@ struct MapKeyHash {
 };
 constexpr size_t kMapCacheMax = 4096;   // entries kept per host thread before the cache starts over
 
-// bf16 tensor with rank (<= 3) dims (innermost first), 128B swizzle, zero fill
-static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-                     const uint32_t* box) {
+bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+              const uint32_t* box, bool bytes) {
   MapKey k;
   std::memset(&k, 0, sizeof(k));   // padding too: keys compare as bytes
   k.base = base;
   k.rank = rank;
+  k.bytes = bytes ? 1u : 0u;
   for (int i = 0; i < rank; ++i) {
     k.dims[i] = dims[i];
     k.box[i] = box[i];
@@ -145,7 +140,7 @@ static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
   auto fn = encode_fn();
   if (!fn) return false;
   uint32_t elem_strides[5] = {1, 1, 1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides_bytes, box,
+  CUresult r = fn(m, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides_bytes, box,
                   elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return false;
@@ -156,7 +151,7 @@ static bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t*
 
 // ------------------------------------------------------------ helpers
 
-static int num_sms() {
+int num_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
   thread_local int known[kMaxDevices] = {};   // per device, read once per host thread
@@ -167,10 +162,6 @@ static int num_sms() {
   }
   return known[dev];
 }
-
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 struct Plan {
   int tiles_per_split = 1;
@@ -254,7 +245,7 @@ static Plan plan_split_uncached(const rag_batch& b, int num_kv_heads, int group,
   return pl;
 }
 
-static rag_status check_pool(const rag_kv_pool* pool) {
+rag_status check_pool(const rag_kv_pool* pool) {
   if (!pool || !pool->k || !pool->v) return RAG_ERR_INVALID_ARG;
   if (!aligned16(pool->k) || !aligned16(pool->v)) return RAG_ERR_INVALID_ARG;
   if (pool->page_size != kPage) return RAG_ERR_UNSUPPORTED;
@@ -271,7 +262,7 @@ static rag_status check_pool(const rag_kv_pool* pool) {
   return RAG_OK;
 }
 
-static rag_status check_batch(const rag_batch* b) {
+rag_status check_batch(const rag_batch* b) {
   if (!b) return RAG_ERR_INVALID_ARG;
   if (b->num_requests < 0 || b->num_requests > kMaxRequests) return RAG_ERR_UNSUPPORTED;
   if (b->num_chunks < 0 || b->num_page_refs < 0 || b->total_q < 0 || b->total_doc < 0 || b->max_q < 0 ||
@@ -286,7 +277,7 @@ static rag_status check_batch(const rag_batch* b) {
   return RAG_OK;
 }
 
-static BatchDev to_dev(const rag_batch& b) {
+BatchDev to_dev(const rag_batch& b) {
   BatchDev d;
   d.req_chunk_off = b.req_chunk_off;
   d.chunk_doc_off = b.chunk_doc_off;

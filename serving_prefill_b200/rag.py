@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librag.so")
 RAG_BF16, RAG_F32 = 0, 1
 PAGE_SIZE = 16
 KERNEL_KINDS = ("pool_write", "attn", "combine", "impact", "topk", "simt_attn", "simt_impact", "rc_plan", "rc_copy",
-                "rc_gemm", "rope_table", "kv_decode", "attn_dec")
+                "rc_gemm", "rope_table", "kv_decode", "attn_dec", "kv_append", "kv8_append", "rope_cos_sin")
 
 STATUS = {
     0: "ok", 1: "invalid argument", 2: "inconsistent shape", 3: "page id outside the pool",
@@ -51,7 +51,21 @@ class RagBatch(ctypes.Structure):
                 ("chunk_page_off", c_void_p), ("page_ids", c_void_p), ("q_off", c_void_p)]
 
 
+class RagKV8Pool(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("num_layers", c_int32), ("num_pages", c_int32), ("num_kv_heads", c_int32), ("page_size", c_int32),
+                ("head_dim", c_int32)]
+
+
+class RagAppend(ctypes.Structure):
+    _fields_ = [("n_seqs", c_int32), ("total_new", c_int32), ("total_pages", c_int32), ("tok_off", c_void_p),
+                ("start", c_void_p), ("page_off", c_void_p), ("page_ids", c_void_p), ("pos0", c_void_p)]
+
+
 _lib = None
+
+_APPEND_ARGS = [c_int32, POINTER(RagAppend), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32, c_void_p,
+                c_int64, c_int32, c_void_p, c_void_p, c_void_p]
 
 EXPORTS = {
     "rag_abi_version": (c_int32, []),
@@ -77,6 +91,9 @@ EXPORTS = {
     "rag_selftest_wait_timeout": (c_int32, [c_void_p, c_int64, c_void_p]),
     "rag_kv_decode": (c_int32, [POINTER(RagKVPool), c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int32,
                                 c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "rag_rope_cos_sin": (c_int32, [c_double, c_int32, c_int32, c_void_p, c_void_p]),
+    "rag_kv_append": (c_int32, [POINTER(RagKVPool)] + _APPEND_ARGS),
+    "rag_kv8_append": (c_int32, [POINTER(RagKV8Pool)] + _APPEND_ARGS),
     "rag_recompute_plan_size": (c_size_t, [POINTER(RagBatch), c_int32]),
     "rag_recompute_plan": (c_int32, [POINTER(RagBatch), c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
                                      c_void_p, c_void_p, c_size_t, c_void_p]),
@@ -145,6 +162,30 @@ class KVPool:
         return self.c.num_kv_heads
 
 
+class KV8Pool:
+    """The paged pool held in 8 bits: e4m3 codes [layers][pages][kv_heads][16][128]
+    for K and V, and one fp32 scale [layers][pages][kv_heads] for each (value =
+    code * scale). rag_kv8_append writes it, rag_kv8_attn reads it."""
+
+    def __init__(self, num_layers, num_pages, num_kv_heads, head_dim=128, device="cuda", k=None, v=None,
+                 k_scale=None, v_scale=None):
+        shape = (num_layers, num_pages, num_kv_heads, PAGE_SIZE, head_dim)
+        dt = torch.float8_e4m3fn
+        self.k = torch.zeros(shape, dtype=dt, device=device) if k is None else k
+        self.v = torch.zeros(shape, dtype=dt, device=device) if v is None else v
+        self.k_scale = torch.ones(shape[:3], device=device) if k_scale is None else k_scale
+        self.v_scale = torch.ones(shape[:3], device=device) if v_scale is None else v_scale
+        for t, sh, d in ((self.k, shape, dt), (self.v, shape, dt), (self.k_scale, shape[:3], torch.float32),
+                         (self.v_scale, shape[:3], torch.float32)):
+            assert tuple(t.shape) == sh and t.dtype == d and t.is_contiguous() and t.device == self.k.device
+        self.c = RagKV8Pool(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                            num_layers, num_pages, num_kv_heads, PAGE_SIZE, head_dim)
+
+    @property
+    def num_kv_heads(self):
+        return self.c.num_kv_heads
+
+
 # --------------------------------------------------------------------------- batch
 
 class Batch:
@@ -176,6 +217,36 @@ class Batch:
     @property
     def total_doc(self):
         return self.c.total_doc
+
+
+class Append:
+    """Which sequences one append call grows (rag_append): int32 arrays, moved to
+    the device if they are not there yet. total_new bounds the rows of k, v and
+    q (the last entry of tok_off when that is on the host and total_new is not
+    given)."""
+
+    def __init__(self, tok_off, start, page_off, page_ids, pos0=None, total_new=None, device="cuda"):
+        if total_new is None:
+            if isinstance(tok_off, torch.Tensor) and tok_off.is_cuda:
+                raise ValueError("total_new is needed when tok_off is on the device")
+            total_new = int(tok_off[-1])
+
+        def dev(x):
+            t = torch.as_tensor(x, dtype=torch.int32)
+            t = t if t.is_cuda else t.to(device)
+            if t.dim() != 1 or not t.is_contiguous():
+                raise ValueError("the arrays of an Append are one-dimensional and contiguous")
+            return t if t.numel() else torch.zeros(1, dtype=torch.int32, device=t.device)
+
+        n, n_pages = len(start), len(page_ids)
+        if len(tok_off) != n + 1 or len(page_off) != n + 1 or (pos0 is not None and len(pos0) != n):
+            raise ValueError("tok_off and page_off have one entry more than start, pos0 as many")
+        self.dev = [dev(x) for x in (tok_off, start, page_off, page_ids)] + [None if pos0 is None else dev(pos0)]
+        self.c = RagAppend(n, total_new, n_pages, *[None if t is None else t.data_ptr() for t in self.dev])
+
+    @property
+    def total_new(self):
+        return self.c.total_new
 
 
 # --------------------------------------------------------------------------- entry points
@@ -272,6 +343,66 @@ def rag_kv_decode(pool: KVPool, layer: int, chunk_tok_off: torch.Tensor, chunk_p
                                _ptr(chunk_page_off), _ptr(page_ids), page_ids.numel(), bits, _ptr(codes_k),
                                _ptr(codes_v), _ptr(scale_k), _ptr(offset_k), _ptr(scale_v), _ptr(offset_v),
                                _ptr(device_err), _stream(stream)), "rag_kv_decode")
+
+
+def _need(ok: bool, status: int, where: str):
+    if not ok:
+        raise RagError(status, where)
+
+
+def _on(t: torch.Tensor, stream):
+    """The stream to launch on: the one given, or the current one of the tensor's
+    device. The library launches on the current device, so it has to be that one."""
+    if t.device.index != torch.cuda.current_device():
+        raise RagError(1, f"the tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def rag_rope_cos_sin(base: float, head_dim: int, n_pos: int, device="cuda", stream=None) -> torch.Tensor:
+    """Table of rotations [n_pos][head_dim / 2][2] = (cos, sin) of p * base^(-2j/head_dim)."""
+    table = torch.empty(max(n_pos, 1), max(head_dim, 2) // 2, 2, device=device)
+    _check(lib().rag_rope_cos_sin(base, head_dim, n_pos, _ptr(table), _on(table, stream)), "rag_rope_cos_sin")
+    return table[:n_pos]
+
+
+def _append(fn, where, pool, dtype, layer, seqs, k, v, rope, q, q_out, device_err, stream):
+    rows, dim, dev = seqs.c.total_new, pool.c.head_dim, pool.k.device
+
+    def strided(t, heads):
+        _need(t.dim() == 3 and t.shape[0] >= rows and t.shape[2] == dim and (heads is None or t.shape[1] == heads), 2, where)
+        _need(t.dtype == dtype and t.device == dev and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == dim), 1, where)
+        return max(t.stride(0), t.shape[1] * dim) if t.shape[0] <= 1 else t.stride(0)
+
+    ks, vs = strided(k, pool.c.num_kv_heads), strided(v, pool.c.num_kv_heads)
+    _need((q is None) == (q_out is None), 1, where)
+    qs = hq = 0
+    if q is not None:
+        qs, hq = strided(q, None), q.shape[1]
+        _need(q_out.shape == q.shape and q_out.dtype == dtype and q_out.is_contiguous() and q_out.device == dev, 2, where)
+    n_pos = 0
+    if rope is not None:
+        n_pos = rope.shape[0]
+        _need(tuple(rope.shape[1:]) == (dim // 2, 2) and rope.dtype == torch.float32 and rope.is_contiguous()
+              and rope.device == dev, 2, where)
+    _check(fn(ctypes.byref(pool.c), layer, ctypes.byref(seqs.c), _ptr(k), ks, _ptr(v), vs, _ptr(rope), n_pos, _ptr(q),
+              qs, hq, _ptr(q_out), _ptr(device_err), _on(k, stream)), where)
+
+
+def rag_kv_append(pool: KVPool, layer: int, seqs: Append, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor = None,
+                  q: torch.Tensor = None, q_out: torch.Tensor = None, device_err: torch.Tensor = None, stream=None):
+    """Append new tokens' k, v [rows][kv_heads][head_dim] (rows may be strided, as
+    slices of a fused projection are) to their sequences' pages, K rotated by the
+    table's rows; q, if given, is rotated into the dense q_out."""
+    _append(lib().rag_kv_append, "rag_kv_append", pool, pool.k.dtype, layer, seqs, k, v, rope, q, q_out, device_err,
+            stream)
+
+
+def rag_kv8_append(pool: KV8Pool, layer: int, seqs: Append, k: torch.Tensor, v: torch.Tensor,
+                   rope: torch.Tensor = None, q: torch.Tensor = None, q_out: torch.Tensor = None,
+                   device_err: torch.Tensor = None, stream=None):
+    """rag_kv_append into an 8-bit pool: bf16 k, v (and q), quantised on the way."""
+    _append(lib().rag_kv8_append, "rag_kv8_append", pool, torch.bfloat16, layer, seqs, k, v, rope, q, q_out,
+            device_err, stream)
 
 
 def rag_recompute_plan_size(batch: Batch, k_cap: int) -> int:

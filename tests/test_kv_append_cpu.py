@@ -1,0 +1,105 @@
+"""Refusals of the append entry points, without a GPU: everything the host can
+see is rejected before a launch."""
+
+import ctypes
+
+import pytest
+import torch
+
+import serving_prefill_b200 as sp
+from serving_prefill_b200.rag import RagAppend, RagKV8Pool, RagKVPool, lib
+
+INVALID, SHAPE, UNSUPPORTED = 1, 2, 4
+
+
+def pool16(dtype=0, head_dim=128, layers=2, heads=8):
+    return RagKVPool(0x10000, 0x20000, layers, 64, heads, 16, head_dim, dtype)
+
+
+def pool8(head_dim=128, page=16, layers=2, pages=64, k=0x10000, ks=0x30000):
+    return RagKV8Pool(k, 0x20000, ks, 0x40000, layers, pages, 8, page, head_dim)
+
+
+def seqs(n=2, total=10, pages=4, tok=0x1000, start=0x2000, po=0x3000, pid=0x4000, pos0=None):
+    return RagAppend(n, total, pages, tok, start, po, pid, pos0)
+
+
+def call(pool, s, fn=None, layer=0, k=0x50000, ks=1024, v=0x60000, vs=1024, rope=0x70000, n_pos=100, q=0x80000,
+         qs=4096, hq=32, q_out=0x90000):
+    fn = fn or (lib().rag_kv8_append if isinstance(pool, RagKV8Pool) else lib().rag_kv_append)
+    return fn(ctypes.byref(pool) if pool is not None else None, layer, ctypes.byref(s) if s is not None else None, k, ks,
+              v, vs, rope, n_pos, q, qs, hq, q_out, None, None)
+
+
+@pytest.mark.parametrize("pool", [pool16(), pool8()], ids=["bf16", "e4m3"])
+def test_arguments_are_refused_before_a_launch(pool):
+    assert call(pool, None) == INVALID
+    for bad in (dict(layer=2), dict(layer=-1), dict(k=None), dict(v=None), dict(k=0x50008), dict(v=0x60004),
+                dict(rope=0x70008), dict(q=0x80004), dict(q_out=0x90008), dict(q_out=None), dict(q=None),
+                dict(n_pos=0), dict(ks=1028), dict(vs=1025), dict(qs=4100), dict(q=0x80000, q_out=0x80000, qs=6144)):
+        assert call(pool, seqs(), **bad) == INVALID, bad
+    for bad in (dict(ks=1016), dict(vs=0), dict(qs=4088), dict(hq=0)):
+        assert call(pool, seqs(), **bad) == SHAPE, bad
+    for s in (seqs(tok=None), seqs(start=None), seqs(po=None), seqs(pid=None)):
+        assert call(pool, s) == INVALID
+    for s in (seqs(n=-1), seqs(total=-1), seqs(pages=-1)):
+        assert call(pool, s) == SHAPE
+    assert call(pool, seqs(n=65537)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("pool", [pool16(), pool8(), pool16(dtype=1, head_dim=64)], ids=["bf16", "e4m3", "f32"])
+def test_an_empty_call_does_nothing(pool):
+    assert call(pool, seqs(n=0)) == 0
+    assert call(pool, seqs(total=0)) == 0
+
+
+def test_pools_are_checked():
+    assert call(None, seqs(), fn=lib().rag_kv8_append) == INVALID
+    assert call(None, seqs(), fn=lib().rag_kv_append) == INVALID
+    assert call(pool8(head_dim=64), seqs()) == UNSUPPORTED
+    assert call(pool8(page=32), seqs()) == UNSUPPORTED
+    assert call(pool8(k=0x10001), seqs()) == INVALID
+    assert call(pool8(ks=None), seqs()) == INVALID
+    assert call(pool8(ks=0x30002), seqs()) == INVALID
+    assert call(pool8(layers=0), seqs()) == SHAPE
+    assert call(pool8(layers=1 << 12, pages=1 << 12), seqs()) == UNSUPPORTED   # 2^27 page blocks
+    assert call(pool16(head_dim=64), seqs()) == UNSUPPORTED                    # bf16 needs head_dim 128
+
+
+def test_table_of_rotations_is_checked():
+    f = lib().rag_rope_cos_sin
+    assert f(1.0, 128, 10, 0x1000, None) == INVALID
+    assert f(float("inf"), 128, 10, 0x1000, None) == INVALID
+    assert f(1e4, 128, 10, None, None) == INVALID
+    assert f(1e4, 128, 10, 0x1008, None) == INVALID
+    assert f(1e4, 128, -1, 0x1000, None) == INVALID
+    assert f(1e4, 96, 10, 0x1000, None) == UNSUPPORTED
+    assert f(1e4, 128, 0, 0x1000, None) == 0
+
+
+def test_append_arrays_are_checked():
+    with pytest.raises(ValueError):
+        sp.Append([0, 1], [0, 0], [0, 1], [0], device="cpu")
+    with pytest.raises(ValueError):
+        sp.Append([0, 1], [0], [0, 1], [0], pos0=[1, 2], device="cpu")
+    with pytest.raises(ValueError):
+        sp.Append(torch.tensor([[0, 1]]).int(), [0], [0, 1], [0], total_new=1, device="cpu")
+    a = sp.Append([0, 3, 7], [0, 5], [0, 1, 2], [4, 9], device="cpu")
+    assert (a.c.n_seqs, a.total_new, a.c.total_pages, a.c.pos0) == (2, 7, 2, None)
+
+
+def test_binding_checks_shapes_types_and_strides():
+    pool = sp.KV8Pool(1, 4, 2, device="cpu")
+    s = sp.Append([0, 3], [0], [0, 1], [2], device="cpu")
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    for bad in (k[:2], k[:, :1], k[:, :, :64], k.float(), torch.zeros(3, 128, 2, dtype=torch.bfloat16).transpose(1, 2)):
+        with pytest.raises(sp.RagError):
+            sp.rag_kv8_append(pool, 0, s, bad, k)
+        with pytest.raises(sp.RagError):
+            sp.rag_kv8_append(pool, 0, s, k, bad)
+    with pytest.raises(sp.RagError):
+        sp.rag_kv8_append(pool, 0, s, k, k, q=k)                              # no q_out
+    with pytest.raises(sp.RagError):
+        sp.rag_kv8_append(pool, 0, s, k, k, rope=torch.zeros(5, 32, 2))       # a table of another head_dim
+    with pytest.raises(AssertionError):
+        sp.KV8Pool(1, 4, 2, device="cpu", k=torch.zeros(1, 4, 2, 16, 128))
