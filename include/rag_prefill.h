@@ -427,7 +427,9 @@ RAG_API rag_status rag_kv_append(const rag_kv_pool* pool, int32_t layer, const r
  * k, v             [num_layers][num_pages][num_kv_heads][16][128] e4m3 codes
  * k_scale, v_scale [num_layers][num_pages][num_kv_heads] fp32
  * value = code * scale of its page and head. rag_kv8_append keeps the scales
- * powers of two, at least 2^-24. */
+ * powers of two, at least 2^-24; the attention takes any positive finite scale
+ * (of V: at most 128, since V enters the product with the weights as fp16).
+ * The codes 0x7f and 0xff (nan) must not stand in slots that hold tokens. */
 typedef struct {
   void* k;
   void* v;
@@ -456,6 +458,38 @@ RAG_API rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const
                                   int64_t k_stride, const void* v, int64_t v_stride, const float* rope,
                                   int32_t n_pos, const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
                                   int32_t* device_err, void* stream);
+
+/* Bytes of workspace rag_kv8_attn needs (0 on invalid arguments). Zero it once
+ * with rag_workspace_init; rag_last_device_error reads its error word. Calls
+ * that may overlap need a workspace each. */
+RAG_API size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch* batch, int32_t num_q_heads);
+
+/* Attention of every request's query tokens over the request's pages of an
+ * 8-bit pool: O[j,h] = sum_i softmax_i(scale * Q[j,h] . K_i) V_i over the
+ * request's N cached tokens in chunk-list order. All keys come from the pool:
+ * the query tokens' own K, V are appended first (as the last tokens of the
+ * request's last chunk), and causal != 0 lets query token j of n_q see the keys
+ * i <= N - n_q + j; causal == 0 shows every key to every token. A query token
+ * that sees no key gets O = 0 and row_lse = -inf.
+ * The batch's device arrays may change between calls, or between replays of a
+ * captured call, within the host totals and maxima of `batch`, which then are
+ * capacities.
+ * q       [total_q][num_q_heads][128] bf16, device
+ * o       [total_q][num_q_heads][128] bf16
+ * row_lse optional [total_q][num_q_heads] fp32
+ * num_q_heads / num_kv_heads may be any whole number up to 128. sm_scale <= 0
+ * selects 1 / sqrt(128).
+ * Precision: Q enters the product as two e4m3 parts per value under a
+ * power-of-two scale per row (together at least the 8 bits of a bf16 value down
+ * to 2^-14 of the row's largest, 2^-18 of it absolute), K as its codes, with
+ * fp32 sums; the softmax runs in fp32; the weights enter the second product in
+ * at least 11 bits, V exactly, with fp32 sums.
+ * The workspace's error word collects page, geometry and timeout errors as
+ * rag_fused_prefill_attn's, and RAG_ERR_RANGE for a scale outside the range
+ * above (it is taken as 1). */
+RAG_API rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch* batch, const void* q,
+                                int32_t num_q_heads, float sm_scale, int32_t causal, void* o, float* row_lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronise `stream`, read and clear the workspace error word. Returns
  * RAG_OK when the device reported nothing, else the most severe of
@@ -488,8 +522,8 @@ RAG_API int64_t rag_launch_count(void);
  * 2 split combine, 3 impact, 4 top-k, 5 fp32 attention, 6 fp32 impact,
  * 7 recompute plan, 8 recompute page copy, 9 recompute projection,
  * 10 RoPE table, 11 KV decode, 12 attention of query blocks of at most 16
- * rows, e.g. decode steps, 13 append, 14 8-bit append, 15 table of rotations)
- * into
+ * rows, e.g. decode steps, 13 append, 14 8-bit append, 15 table of rotations,
+ * 16 8-bit attention, 17 its split combine, 18 its query split) into
  * the first n_kinds entries of ms and launches (either may be NULL), and
  * resets the record. */
 RAG_API void rag_profile_enable(int32_t on);

@@ -19,6 +19,8 @@ from .rag import (  # noqa: F401
     rag_fused_prefill_attn_rope,
     rag_impact_topk,
     rag_kv8_append,
+    rag_kv8_attn,
+    rag_kv8_workspace_size,
     rag_kv_append,
     rag_kv_decode,
     rag_kv_pool_write,

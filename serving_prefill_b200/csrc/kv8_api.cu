@@ -72,7 +72,77 @@ static rag_status check_append(AppendParams& p, int elem, int num_layers, int la
   return RAG_OK;
 }
 
+// ------------------------------------------------------------ attention
+
+struct Kv8Plan {
+  int tiles_per_split, direct, grid, toks_per_block, item_rows;
+  int64_t max_items;
+};
+
+// Split the key tiles of every unit (request, KV head, block of query tokens)
+// so that the work fills the SMs. Every split length is tried; the cost of one
+// is, for one request (alike items), ceil(items / SMs) of them after one
+// another, for several the list-scheduling bound (average load per SM plus one
+// longest item), an item's start and end counted as two tiles.
+static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
+  Kv8Plan pl;
+  pl.toks_per_block = kQTiles * (kBM / group);
+  pl.item_rows = kFwdRows;
+  const double overhead = 2.0;
+  const int B = std::max(1, b.num_requests);
+  const int tiles_max = std::max(1, cdiv(b.max_pages, kPagesPerTile));
+  const int rt_avg = std::max(1, cdiv(cdiv(b.total_q, B), pl.toks_per_block));
+  const int tiles_avg = std::max(1, cdiv(cdiv(b.num_page_refs, B), kPagesPerTile));
+  const double units = double(num_kv_heads) * B * rt_avg;
+  double best = 1e300;
+  int best_ts = tiles_max;
+  for (int ts = std::min(2, tiles_max); ts <= tiles_max; ++ts) {
+    const double items = units * cdiv(tiles_avg, ts);
+    const double cost = B == 1 ? std::ceil(items / sms) * (std::min(ts, tiles_avg) + overhead)
+                               : (units * tiles_avg + items * overhead) / sms + std::min(ts, tiles_avg) + overhead;
+    if (cost < best + 1e-9) {   // ties go to the longer split (fewer partial rows)
+      best = cost;
+      best_ts = ts;
+    }
+  }
+  pl.tiles_per_split = best_ts;
+  pl.direct = best_ts >= tiles_max ? 1 : 0;
+  const int64_t rt_bound = cdiv(b.total_q, pl.toks_per_block) + int64_t(b.num_requests);
+  pl.max_items = int64_t(num_kv_heads) * rt_bound * cdiv(tiles_max, best_ts);
+  pl.grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, pl.max_items)));
+  return pl;
+}
+
+// Workspace (bytes, each region 256-aligned): error word, item prefix, split
+// queries, their row scales, partial rows (none when a unit is one item).
+struct Kv8Ws {
+  size_t off_prefix, off_qs, off_qscale, off_part, total;
+};
+static Kv8Ws ws_kv8(const rag_batch& b, int num_q_heads, const Kv8Plan& pl) {
+  Kv8Ws w;
+  const size_t rows = size_t(b.total_q) * num_q_heads;
+  size_t at = 256;
+  w.off_prefix = at; at = align256(at + sizeof(int32_t) * (size_t(b.num_requests) + 1));
+  w.off_qs = at; at = align256(at + rows * 2 * kHeadDim);
+  w.off_qscale = at; at = align256(at + rows * sizeof(float));
+  w.off_part = at;
+  if (!pl.direct) at = align256(at + size_t(pl.max_items) * pl.item_rows * kPartStride * sizeof(float));
+  w.total = at;
+  return w;
+}
+
+static rag_status check_kv8_attn(const rag_kv8_pool* pool, const rag_batch* batch, int32_t num_q_heads) {
+  rag_status st = check_pool8(pool);
+  if (st != RAG_OK) return st;
+  st = check_batch(batch);
+  if (st != RAG_OK) return st;
+  if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0) return RAG_ERR_SHAPE;
+  if (num_q_heads / pool->num_kv_heads > kBM) return RAG_ERR_UNSUPPORTED;
+  return RAG_OK;
+}
+
 }  // namespace rag
+
 
 using namespace rag;
 
@@ -140,6 +210,87 @@ rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_app
   cudaError_t e = launch_kv8_append(p, int(kv_blocks + q_blocks), s);
   ls.done(e);
   return e == cudaSuccess ? RAG_OK : RAG_ERR_CUDA;
+}
+
+size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch* batch, int32_t num_q_heads) {
+  if (check_kv8_attn(pool, batch, num_q_heads) != RAG_OK) return 0;
+  return ws_kv8(*batch, num_q_heads, plan_kv8(*batch, pool->num_kv_heads, num_q_heads / pool->num_kv_heads, num_sms())).total;
+}
+
+rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch* batch, const void* q,
+                        int32_t num_q_heads, float sm_scale, int32_t causal, void* o, float* row_lse, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  const rag_status st = check_kv8_attn(pool, batch, num_q_heads);
+  if (st != RAG_OK) return st;
+  if (layer < 0 || layer >= pool->num_layers) return RAG_ERR_INVALID_ARG;
+  const rag_batch& b = *batch;
+  if (b.total_q > 0 && (!q || !o)) return RAG_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(row_lse) & 3u)) return RAG_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale)) return RAG_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return RAG_ERR_WORKSPACE;
+  const int H = pool->num_kv_heads, G = num_q_heads / H;
+  const Kv8Plan pl = plan_kv8(b, H, G, num_sms());
+  const Kv8Ws ws = ws_kv8(b, num_q_heads, pl);
+  if (workspace_bytes < ws.total) return RAG_ERR_WORKSPACE;
+  if (b.num_requests == 0 || b.total_q == 0) return RAG_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  Kv8Params p = {};
+  p.batch = to_dev(b);
+  p.num_pages = pool->num_pages;
+  p.num_kv_heads = H;
+  p.num_q_heads = num_q_heads;
+  p.group = G;
+  p.layer = layer;
+  p.tiles_per_split = pl.tiles_per_split;
+  p.toks_per_block = pl.toks_per_block;
+  p.item_rows = pl.item_rows;
+  p.direct = pl.direct;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(float(kHeadDim))) * 1.4426950408889634f;
+  p.k_scale = pool->k_scale;
+  p.v_scale = pool->v_scale;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.qs = base + ws.off_qs;
+  p.qscale = reinterpret_cast<float*>(base + ws.off_qscale);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.row_lse = row_lse;
+  p.part = reinterpret_cast<float*>(base + ws.off_part);
+  p.item_prefix = reinterpret_cast<int32_t*>(base + ws.off_prefix);
+  p.err = reinterpret_cast<int32_t*>(base);
+  p.max_items = pl.max_items;
+
+  CUtensorMap tm_q, tm_k, tm_v;
+  {
+    const uint64_t dq[3] = {2u * kHeadDim, uint64_t(num_q_heads), uint64_t(b.total_q)};
+    const uint64_t sq[2] = {2u * kHeadDim, uint64_t(num_q_heads) * 2 * kHeadDim};
+    const uint32_t bq[3] = {uint32_t(kHeadDim), uint32_t(G), uint32_t(kBM / G)};
+    const uint64_t dp[2] = {uint64_t(kHeadDim), uint64_t(pool->num_layers) * pool->num_pages * H * kPage};
+    const uint64_t sp[1] = {uint64_t(kHeadDim)};
+    const uint32_t bp[2] = {uint32_t(kHeadDim), uint32_t(kPage)};
+    if (!make_map(&tm_k, pool->k, 2, dp, sp, bp, true) || !make_map(&tm_v, pool->v, 2, dp, sp, bp, true) ||
+        !make_map(&tm_q, p.qs, 3, dq, sq, bq, true))
+      return RAG_ERR_CUDA;
+  }
+  {
+    LaunchScope ls(kKindKv8SplitQ, s);
+    cudaError_t e = launch_kv8_split_q(p, s);
+    ls.done(e);
+    if (e != cudaSuccess) return RAG_ERR_CUDA;
+  }
+  {
+    LaunchScope ls(kKindKv8Attn, s);
+    cudaError_t e = launch_kv8_fwd(tm_q, tm_k, tm_v, p, pl.grid, s);
+    ls.done(e);
+    if (e != cudaSuccess) return RAG_ERR_CUDA;
+  }
+  if (!pl.direct) {
+    LaunchScope ls(kKindKv8Combine, s);
+    cudaError_t e = launch_kv8_combine(p, b.max_q, s);
+    ls.done(e);
+    if (e != cudaSuccess) return RAG_ERR_CUDA;
+  }
+  return RAG_OK;
 }
 
 }  // extern "C"

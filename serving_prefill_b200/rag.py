@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librag.so")
 RAG_BF16, RAG_F32 = 0, 1
 PAGE_SIZE = 16
 KERNEL_KINDS = ("pool_write", "attn", "combine", "impact", "topk", "simt_attn", "simt_impact", "rc_plan", "rc_copy",
-                "rc_gemm", "rope_table", "kv_decode", "attn_dec", "kv_append", "kv8_append", "rope_cos_sin")
+                "rc_gemm", "rope_table", "kv_decode", "attn_dec", "kv_append", "kv8_append", "rope_cos_sin",
+                "kv8_attn", "kv8_combine", "kv8_split_q")
 
 STATUS = {
     0: "ok", 1: "invalid argument", 2: "inconsistent shape", 3: "page id outside the pool",
@@ -94,6 +95,9 @@ EXPORTS = {
     "rag_rope_cos_sin": (c_int32, [c_double, c_int32, c_int32, c_void_p, c_void_p]),
     "rag_kv_append": (c_int32, [POINTER(RagKVPool)] + _APPEND_ARGS),
     "rag_kv8_append": (c_int32, [POINTER(RagKV8Pool)] + _APPEND_ARGS),
+    "rag_kv8_workspace_size": (c_size_t, [POINTER(RagKV8Pool), POINTER(RagBatch), c_int32]),
+    "rag_kv8_attn": (c_int32, [POINTER(RagKV8Pool), c_int32, POINTER(RagBatch), c_void_p, c_int32, c_float, c_int32,
+                               c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "rag_recompute_plan_size": (c_size_t, [POINTER(RagBatch), c_int32]),
     "rag_recompute_plan": (c_int32, [POINTER(RagBatch), c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
                                      c_void_p, c_void_p, c_size_t, c_void_p]),
@@ -277,8 +281,17 @@ def rag_workspace_size(pool: KVPool, batch: Batch, num_q_heads: int) -> int:
     return n
 
 
-def new_workspace(pool: KVPool, batch: Batch, num_q_heads: int, device="cuda", stream=None) -> torch.Tensor:
-    n = rag_workspace_size(pool, batch, num_q_heads)
+def rag_kv8_workspace_size(pool: KV8Pool, batch: Batch, num_q_heads: int) -> int:
+    n = lib().rag_kv8_workspace_size(ctypes.byref(pool.c), ctypes.byref(batch.c), num_q_heads)
+    if n == 0:
+        raise RagError(1, "rag_kv8_workspace_size")
+    return n
+
+
+def new_workspace(pool, batch: Batch, num_q_heads: int, device="cuda", stream=None) -> torch.Tensor:
+    """Workspace for rag_fused_prefill_attn (a KVPool) or rag_kv8_attn (a KV8Pool)."""
+    size = rag_kv8_workspace_size if isinstance(pool, KV8Pool) else rag_workspace_size
+    n = size(pool, batch, num_q_heads)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     _check(lib().rag_workspace_init(_ptr(ws), n, _stream(stream)), "rag_workspace_init")
     return ws
@@ -403,6 +416,22 @@ def rag_kv8_append(pool: KV8Pool, layer: int, seqs: Append, k: torch.Tensor, v: 
     """rag_kv_append into an 8-bit pool: bf16 k, v (and q), quantised on the way."""
     _append(lib().rag_kv8_append, "rag_kv8_append", pool, torch.bfloat16, layer, seqs, k, v, rope, q, q_out,
             device_err, stream)
+
+
+def rag_kv8_attn(pool: KV8Pool, layer: int, batch: Batch, q: torch.Tensor, o: torch.Tensor, workspace: torch.Tensor,
+                 causal: bool = True, row_lse: torch.Tensor = None, sm_scale: float = 0.0, stream=None):
+    """Attention of the query tokens q [total_q][num_q_heads][128] (bf16) over their
+    requests' pages of an 8-bit pool, into o; causal: query token j of n_q sees
+    the first N - n_q + j + 1 of the request's N cached tokens."""
+    where, dev = "rag_kv8_attn", pool.k.device
+    _need(q.dim() == 3 and q.shape[0] >= batch.c.total_q and q.shape[2] == 128 and o.shape == q.shape, 2, where)
+    for t, dt in ((q, torch.bfloat16), (o, torch.bfloat16), (row_lse, torch.float32)):
+        _need(t is None or (t.dtype == dt and t.is_contiguous() and t.device == dev), 1, where)
+    _need(row_lse is None or tuple(row_lse.shape) == tuple(q.shape[:2]), 2, where)
+    _need(workspace.device == dev and workspace.is_contiguous(), 7, where)
+    _check(lib().rag_kv8_attn(ctypes.byref(pool.c), layer, ctypes.byref(batch.c), _ptr(q), q.shape[1], sm_scale,
+                              1 if causal else 0, _ptr(o), _ptr(row_lse), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _on(q, stream)), where)
 
 
 def rag_recompute_plan_size(batch: Batch, k_cap: int) -> int:
