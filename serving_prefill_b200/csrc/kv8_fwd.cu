@@ -231,7 +231,16 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->desc_empty[slot]);
-        if (!active) continue;
+        if (!active) {
+          // The other warpgroup uses S buffer 1 for the odd tiles; follow its
+          // phases one by one. Descriptors run ahead of the products, and a
+          // parity tells only neighbouring phases apart.
+          if (i & 1) {
+            if (!mbar_wait(&ctl->s_full[1], n_sf1 & 1, abort_flag)) { bad = 1; break; }
+            ++n_sf1;
+          }
+          continue;
+        }
         const int sb = single ? (i & 1) : qt;   // S buffer of this step
         const uint32_t s_addr = tmem + lane_off + col_s(sb);
         if (!mbar_wait(&ctl->s_full[sb], (sb ? n_sf1 : n_sf0) & 1, abort_flag)) { bad = 1; break; }
@@ -334,10 +343,8 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       }
       if (bad) break;
       t_glob += n;
-      // completions of s_full[1] that the other warpgroup consumed: the odd
-      // tiles of a one-Q-tile item (warpgroup 0's), every tile of a two-Q-tile
-      // item (warpgroup 1's)
-      if (single && qt == 1) n_sf1 += uint32_t(n) / 2;
+      // completions of s_full[1] that warpgroup 1 consumed in a two-Q-tile item
+      // (all of them by the time O_0 is complete, which comes after the last)
       if (!single && qt == 0) n_sf1 += uint32_t(n);
       if (!active) continue;
 

@@ -58,3 +58,16 @@ def test_short_query_blocks(name, causal):
     case = AttnCase(*SINGLE[name], seed=len(name))
     check(case.run(causal), case.reference(causal))
     assert sp.rag_last_device_error(case.ws) == (0, 0)
+
+
+@pytest.mark.parametrize("seed", [0, 1])
+def test_many_items_a_block_of_every_kind(seed):
+    """More work items than SMs, one- and two-tile query blocks and single
+    tokens mixed, so that a block walks items of every kind in turn."""
+    import random
+    r = random.Random(seed)
+    reqs = [([r.randint(1, 400) for _ in range(r.randint(1, 5))], r.choice([1, 2, 20, 33, 60, 64, 70, 100, 129]))
+            for _ in range(24)]
+    case = AttnCase(8, 4, reqs, seed=seed)
+    check(case.run(True), case.reference(True))
+    assert sp.rag_last_device_error(case.ws) == (0, 0)
