@@ -523,7 +523,8 @@ RAG_API int64_t rag_launch_count(void);
  * 7 recompute plan, 8 recompute page copy, 9 recompute projection,
  * 10 RoPE table, 11 KV decode, 12 attention of query blocks of at most 16
  * rows, e.g. decode steps, 13 append, 14 8-bit append, 15 table of rotations,
- * 16 8-bit attention, 17 its split combine, 18 its query split) into
+ * 16 8-bit attention, 17 its split combine, 18 its query split,
+ * 19 8-bit attention of at most 16 rows) into
  * the first n_kinds entries of ms and launches (either may be NULL), and
  * resets the record. */
 RAG_API void rag_profile_enable(int32_t on);

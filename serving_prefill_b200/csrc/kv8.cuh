@@ -232,6 +232,9 @@ __device__ __forceinline__ float page_scale_ok(const Kv8Params& p, float s, int 
 cudaError_t launch_kv8_split_q(const Kv8Params&, cudaStream_t);
 cudaError_t launch_kv8_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p,
                            int grid, cudaStream_t stream);
+// query blocks of at most 16 rows
+cudaError_t launch_kv8_decode(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, int grid,
+                              cudaStream_t stream);
 cudaError_t launch_kv8_combine(const Kv8Params& p, int max_q, cudaStream_t stream);
 
 }  // namespace rag

@@ -75,6 +75,7 @@ static rag_status check_append(AppendParams& p, int elem, int num_layers, int la
 // ------------------------------------------------------------ attention
 
 struct Kv8Plan {
+  int decode;   // query blocks of at most 16 rows: the transposed kernel
   int tiles_per_split, direct, grid, toks_per_block, item_rows;
   int64_t max_items;
 };
@@ -86,9 +87,11 @@ struct Kv8Plan {
 // longest item), an item's start and end counted as two tiles.
 static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
   Kv8Plan pl;
-  pl.toks_per_block = kQTiles * (kBM / group);
-  pl.item_rows = kFwdRows;
-  const double overhead = 2.0;
+  pl.decode = int64_t(b.max_q) * group <= 16 ? 1 : 0;
+  pl.toks_per_block = pl.decode ? 16 / group : kQTiles * (kBM / group);
+  pl.item_rows = pl.decode ? 16 : kFwdRows;
+  if (pl.decode) sms *= 2;   // two CTAs share an SM
+  const double overhead = pl.decode ? 4.0 : 2.0;
   const int B = std::max(1, b.num_requests);
   const int tiles_max = std::max(1, cdiv(b.max_pages, kPagesPerTile));
   const int rt_avg = std::max(1, cdiv(cdiv(b.total_q, B), pl.toks_per_block));
@@ -120,7 +123,7 @@ struct Kv8Ws {
 };
 static Kv8Ws ws_kv8(const rag_batch& b, int num_q_heads, const Kv8Plan& pl) {
   Kv8Ws w;
-  const size_t rows = size_t(b.total_q) * num_q_heads;
+  const size_t rows = pl.decode ? 0 : size_t(b.total_q) * num_q_heads;   // the decode kernel splits its own queries
   size_t at = 256;
   w.off_prefix = at; at = align256(at + sizeof(int32_t) * (size_t(b.num_requests) + 1));
   w.off_qs = at; at = align256(at + rows * 2 * kHeadDim);
@@ -262,23 +265,28 @@ rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch
 
   CUtensorMap tm_q, tm_k, tm_v;
   {
-    const uint64_t dq[3] = {2u * kHeadDim, uint64_t(num_q_heads), uint64_t(b.total_q)};
-    const uint64_t sq[2] = {2u * kHeadDim, uint64_t(num_q_heads) * 2 * kHeadDim};
-    const uint32_t bq[3] = {uint32_t(kHeadDim), uint32_t(G), uint32_t(kBM / G)};
     const uint64_t dp[2] = {uint64_t(kHeadDim), uint64_t(pool->num_layers) * pool->num_pages * H * kPage};
     const uint64_t sp[1] = {uint64_t(kHeadDim)};
     const uint32_t bp[2] = {uint32_t(kHeadDim), uint32_t(kPage)};
-    if (!make_map(&tm_k, pool->k, 2, dp, sp, bp, true) || !make_map(&tm_v, pool->v, 2, dp, sp, bp, true) ||
-        !make_map(&tm_q, p.qs, 3, dq, sq, bq, true))
+    if (!make_map(&tm_k, pool->k, 2, dp, sp, bp, true) || !make_map(&tm_v, pool->v, 2, dp, sp, bp, true))
       return RAG_ERR_CUDA;
   }
-  {
-    LaunchScope ls(kKindKv8SplitQ, s);
-    cudaError_t e = launch_kv8_split_q(p, s);
+  if (pl.decode) {
+    LaunchScope ls(kKindKv8Decode, s);
+    cudaError_t e = launch_kv8_decode(tm_k, tm_v, p, pl.grid, s);
     ls.done(e);
     if (e != cudaSuccess) return RAG_ERR_CUDA;
-  }
-  {
+  } else {
+    const uint64_t dq[3] = {2u * kHeadDim, uint64_t(num_q_heads), uint64_t(b.total_q)};
+    const uint64_t sq[2] = {2u * kHeadDim, uint64_t(num_q_heads) * 2 * kHeadDim};
+    const uint32_t bq[3] = {uint32_t(kHeadDim), uint32_t(G), uint32_t(kBM / G)};
+    if (!make_map(&tm_q, p.qs, 3, dq, sq, bq, true)) return RAG_ERR_CUDA;
+    {
+      LaunchScope ls(kKindKv8SplitQ, s);
+      cudaError_t e = launch_kv8_split_q(p, s);
+      ls.done(e);
+      if (e != cudaSuccess) return RAG_ERR_CUDA;
+    }
     LaunchScope ls(kKindKv8Attn, s);
     cudaError_t e = launch_kv8_fwd(tm_q, tm_k, tm_v, p, pl.grid, s);
     ls.done(e);
