@@ -380,7 +380,7 @@ RAG_API rag_status rag_recompute_status(const void* plan, int32_t* counts, void*
  *   page_ids [total_pages]
  *   pos0     [n_seqs]     optional (NULL: 0): position of the sequence's token 0
  * total_new and total_pages bound the prefixes; rows of k, v, q from
- * tok_off[n_seqs] to total_new-1 are padding: not read, and their rows of q_out
+ * tok_off[n_seqs] to total_new-1 are padding: not used, and their rows of q_out
  * are left as they were. A page that receives tokens belongs to one sequence of
  * the call. With fixed arrays whose contents the caller advances on the device,
  * a captured call can be replayed. */
@@ -524,7 +524,7 @@ RAG_API int64_t rag_launch_count(void);
  * 10 RoPE table, 11 KV decode, 12 attention of query blocks of at most 16
  * rows, e.g. decode steps, 13 append, 14 8-bit append, 15 table of rotations,
  * 16 8-bit attention, 17 its split combine, 18 its query split,
- * 19 8-bit attention of at most 16 rows) into
+ * 19 8-bit attention of at most 16 rows, 20 rotation of queries alone) into
  * the first n_kinds entries of ms and launches (either may be NULL), and
  * resets the record. */
 RAG_API void rag_profile_enable(int32_t on);

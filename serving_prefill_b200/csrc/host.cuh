@@ -15,7 +15,7 @@ namespace rag {
 // kernel kinds of the per-kernel timing (rag_profile_collect)
 enum Kind { kKindPoolWrite = 0, kKindAttn, kKindCombine, kKindImpact, kKindTopk, kKindSimtAttn, kKindSimtImpact,
             kKindRcPlan, kKindRcCopy, kKindRcGemm, kKindRope, kKindKvDecode, kKindDecAttn,
-            kKindKvAppend, kKindKv8Append, kKindRopeTable, kKindKv8Attn, kKindKv8Combine, kKindKv8SplitQ, kKindKv8Decode, kNumKinds };
+            kKindKvAppend, kKindKv8Append, kKindRopeTable, kKindKv8Attn, kKindKv8Combine, kKindKv8SplitQ, kKindKv8Decode, kKindRopeQ, kNumKinds };
 
 // Counts one launch and, while profiling is on, brackets it with events.
 struct LaunchScope {

@@ -74,12 +74,15 @@ struct AppendParams {
   const float2* rope;        // [n_pos][head_dim / 2] (cos, sin) or null
   int32_t* err;
   int32_t n_pos, layer, num_pages, num_kv_heads, num_q_heads, head_dim;
-  int32_t tokens_per_block;
+  int32_t tokens_per_block, units_per_block;   // at most 8
+  int32_t heads_split;       // blocks that share a group of units
   int32_t kv_blocks;         // 8-bit pool: blocks that store K and V (the rest rotate q)
 };
 
 cudaError_t launch_kv_append(const AppendParams&, int is_f32, int grid, cudaStream_t);
 cudaError_t launch_kv8_append(const AppendParams&, int grid, cudaStream_t);
+cudaError_t launch_kv8_append_stream(const AppendParams&, int grid, cudaStream_t);
+cudaError_t launch_rope_q(const AppendParams&, int grid, cudaStream_t);
 cudaError_t launch_rope_cos_sin(double base, int head_dim, int n_pos, float2* table, cudaStream_t);
 
 // ------------------------------------------------------------ attention

@@ -13,6 +13,8 @@
 namespace rag {
 
 constexpr int kMaxAppendSeqs = 65536;
+// Page blocks of K an SM from which an 8-bit append streams its rows.
+constexpr int kStreamBlocksPerSm = 8;
 
 static rag_status check_pool8(const rag_kv8_pool* pool) {
   if (!pool || !pool->k || !pool->v || !pool->k_scale || !pool->v_scale) return RAG_ERR_INVALID_ARG;
@@ -202,13 +204,41 @@ rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_app
   p.pool_v = static_cast<uint8_t*>(pool->v);
   p.k_scale = pool->k_scale;
   p.v_scale = pool->v_scale;
-  // units of a call: see kv8_append_kernel
-  const int64_t units = int64_t(seqs->total_new) / kPage + 2 * int64_t(seqs->n_seqs);
-  const int64_t kv_blocks = (units * 2 * p.num_kv_heads + 7) / 8;
-  const int64_t q_blocks = q ? cdiv(seqs->total_new, p.tokens_per_block) : 0;
+  const int64_t units = int64_t(seqs->total_new) / kPage + 2 * int64_t(seqs->n_seqs);   // see kv8_append_kernel
+  const int q_blocks = q ? cdiv(seqs->total_new, p.tokens_per_block) : 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (int64_t(seqs->total_new) / kPage * p.num_kv_heads >= kStreamBlocksPerSm * int64_t(num_sms())) {
+    // many tokens: rows streamed through shared memory, queries in a launch of their own
+    const int slots = 2 * num_sms();
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= 8; ++n) {   // units a block: the fewest rounds of blocks, then the longest blocks
+      const int64_t rounds = cdiv(cdiv(units, n), slots) * int64_t(n);
+      if (rounds <= best) {
+        best = rounds;
+        p.units_per_block = n;
+      }
+    }
+    {
+      LaunchScope ls(kKindKv8Append, s);
+      cudaError_t e = launch_kv8_append_stream(p, cdiv(units, p.units_per_block), s);
+      ls.done(e);
+      if (e != cudaSuccess) return RAG_ERR_CUDA;
+    }
+    if (q) {
+      LaunchScope ls(kKindRopeQ, s);
+      cudaError_t e = launch_rope_q(p, q_blocks, s);
+      ls.done(e);
+      if (e != cudaSuccess) return RAG_ERR_CUDA;
+    }
+    return RAG_OK;
+  }
+  // a block takes several units once the GPU is filled a few times over, and
+  // with few units only 8 page blocks of one, so that no warp takes two
+  p.units_per_block = int(std::max<int64_t>(1, std::min<int64_t>(8, units / (8 * num_sms()))));
+  p.heads_split = units < 4 * num_sms() ? cdiv(2 * p.num_kv_heads, 8) : 1;
+  const int64_t kv_blocks = (units + p.units_per_block - 1) / p.units_per_block * p.heads_split;
   if (kv_blocks + q_blocks >= (int64_t(1) << 31)) return RAG_ERR_UNSUPPORTED;
   p.kv_blocks = int(kv_blocks);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   LaunchScope ls(kKindKv8Append, s);
   cudaError_t e = launch_kv8_append(p, int(kv_blocks + q_blocks), s);
   ls.done(e);

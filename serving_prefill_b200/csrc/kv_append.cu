@@ -41,12 +41,19 @@ struct Tok {
   int32_t live;      // 0: a row behind the last sequence
 };
 
-// Last s with tok_off[s] <= t (0 when there is none).
-__device__ __forceinline__ int seq_of(const AppendSeqs& a, int t) {
-  int lo = 0, hi = a.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.tok_off + mid) <= t) lo = mid; else hi = mid - 1;
+// Last s with key(s) <= x, key rising (0 when there is none), by the whole
+// warp: 32 probes a round, so that up to 32 sequences cost one load's latency
+// instead of five.
+template <typename Key>
+__device__ __forceinline__ int last_at_or_before(int n, int x, int lane, Key key) {
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, lane * step < len && key(at) <= x);
+    const int k = max(__popc(le) - 1, 0);
+    len = min(step, len - k * step);
+    lo += k * step;
   }
   return lo;
 }
@@ -70,15 +77,19 @@ __device__ __forceinline__ Seq load_seq(const AppendSeqs& a, int s) {
   return q;
 }
 
-__device__ __forceinline__ Tok token_of(const AppendParams& p, int t, bool report) {
+// Resolve token t (whole warp; lane 0 reports).
+__device__ __forceinline__ Tok token_of(const AppendParams& p, int t, int lane, bool report) {
   Tok k;
   k.page = -1; k.slot = 0; k.pos = -1; k.tail = 0; k.live = 0;
-  if (t >= p.seqs.total_new || t >= __ldg(p.seqs.tok_off + p.seqs.n_seqs)) return k;
+  report = report && lane == 0 && p.err;
+  const int end = __ldg(p.seqs.tok_off + p.seqs.n_seqs);
+  const int s = last_at_or_before(p.seqs.n_seqs, t, lane, [&](int i) { return __ldg(p.seqs.tok_off + i); });
+  if (t >= p.seqs.total_new || t >= end) return k;
   k.live = 1;
-  const Seq q = load_seq(p.seqs, seq_of(p.seqs, t));
+  const Seq q = load_seq(p.seqs, s);
   const int at = t - q.t0;
   if (!q.ok || at < 0 || at >= q.n) {
-    if (report && p.err) atomicOr(p.err, kDevErrGeometry);
+    if (report) atomicOr(p.err, kDevErrGeometry);
     return k;
   }
   const int i = q.start + at;
@@ -87,151 +98,217 @@ __device__ __forceinline__ Tok token_of(const AppendParams& p, int t, bool repor
     k.pos = 0;
   } else if (pos >= 0 && pos < p.n_pos) {
     k.pos = int32_t(pos);
-  } else if (report && p.err) {
+  } else if (report) {
     atomicOr(p.err, kDevErrGeometry);
   }
   const int page = __ldg(p.seqs.page_ids + q.p0 + i / kPage);
   if (page < 0 || page >= p.num_pages) {
-    if (report && p.err) atomicOr(p.err, kDevErrPage);
+    if (report) atomicOr(p.err, kDevErrPage);
     return k;
   }
   k.page = page;
   k.slot = i % kPage;
-  const bool last = at == q.n - 1;
-  if (last && i - k.slot >= q.start) k.tail = kPage - 1 - k.slot;
+  if (at == q.n - 1 && i - k.slot >= q.start) k.tail = kPage - 1 - k.slot;
   return k;
 }
 
-// The two products' rounding is part of the operator (see above).
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
-  const float na = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
-  const float nb = __fadd_rn(__fmul_rn(b, cs.x), __fmul_rn(a, cs.y));
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return bits_f2(d);
+}
+
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// As fmax3, but a nan comes through.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two pairs turned at once (x of a and b: one pair, y: the next): a c - b s and
+// b c + a s, every product and sum rounded on its own, which is part of the
+// operator (see above). x - y is the fused x + y * -1: that product is exact.
+__device__ __forceinline__ void turn2(float2& a, float2& b, float4 cs) {   // cs: both cosines, both sines
+  const float2 c = make_float2(cs.x, cs.y), sn = make_float2(cs.z, cs.w);
+  const float2 na = ffma2(fmul2(b, sn), make_float2(-1.f, -1.f), fmul2(a, c));
+  const float2 nb = fadd2(fmul2(b, c), fmul2(a, sn));
   a = na;
   b = nb;
 }
 
-// 16 bytes of a row's first half and of its second half as fp32 pairs.
+// A table row in shared memory: the vector (two pairs) that lane c of a row
+// reads j-th lies at [j][c], so that the lanes of a row read neighbouring
+// vectors; in the table they lie 16 N / 2 bytes apart, which costs a cache line
+// a lane (the table's reads then took longer than the rows'). Within a vector
+// the two cosines come first, as the packed products take them.
+__device__ __forceinline__ float4 tab_vec(const float4* at) {
+  const float4 v = __ldg(at);
+  return make_float4(v.x, v.z, v.y, v.w);
+}
+template <int N>
+__device__ __forceinline__ int tab_at(int f, int lanes) { return f % (N / 2) * lanes + f / (N / 2); }
+
+// A row's two 16-byte vectors (one of each half) as they lie in memory.
+struct Raw {
+  uint4 a, b;
+};
+__device__ __forceinline__ Raw load_raw(const uint8_t* at, int half_bytes) {
+  Raw r;
+  r.a = *reinterpret_cast<const uint4*>(at);   // not the read-only path: q may be rotated in place
+  r.b = *reinterpret_cast<const uint4*>(at + half_bytes);
+  return r;
+}
+// 16 bytes of a row as fp32 pairs, and back.
 template <typename T> struct Vec;
 template <> struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  static __device__ __forceinline__ void load(const uint8_t* at, float* x) {
-    const uint4 w = *reinterpret_cast<const uint4*>(at);
+  static __device__ __forceinline__ void unpack(const uint4& w, float2* x) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(u[j] << 16);
-      x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < 4; ++j) x[j] = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
   }
-  static __device__ __forceinline__ void store(uint8_t* at, const float* x) {
-    *reinterpret_cast<uint4*>(at) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  static __device__ __forceinline__ uint4 pack(const float2* x) {
+    return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                      pack_bf16x2(x[3].x, x[3].y));
   }
 };
 template <> struct Vec<float> {
   static constexpr int kN = 4;
-  static __device__ __forceinline__ void load(const uint8_t* at, float* x) {
-    const float4 w = *reinterpret_cast<const float4*>(at);
-    x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
+  static __device__ __forceinline__ void unpack(const uint4& w, float2* x) {
+    x[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    x[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
-  static __device__ __forceinline__ void store(uint8_t* at, const float* x) {
-    *reinterpret_cast<float4*>(at) = make_float4(x[0], x[1], x[2], x[3]);
+  static __device__ __forceinline__ uint4 pack(const float2* x) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
   }
 };
-// V of a bf16 cache is stored as fp16 (saturated, reported).
-__device__ __forceinline__ void store_f16(uint8_t* at, const float* x, bool& over) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) over = over || !(fabsf(x[j]) < 65520.f);
-  *reinterpret_cast<uint4*>(at) = make_uint4(pack_f16x2_sat(x[0], x[1]), pack_f16x2_sat(x[2], x[3]),
-                                             pack_f16x2_sat(x[4], x[5]), pack_f16x2_sat(x[6], x[7]));
-}
 
+// Row turned by the table row at tab (null: as it is); pos < 0: zeros.
 template <typename T>
-__device__ __forceinline__ void rotate_row(const AppendParams& p, int pos, int c, float* a, float* b) {
+__device__ __forceinline__ Raw turn_raw(const float4* tab, int pos, int c, int lanes, const Raw& r) {
   constexpr int N = Vec<T>::kN;
-  if (pos < 0) {
+  if (pos < 0) return Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  if (!tab) return r;
+  float2 a[N / 2], b[N / 2];
+  Vec<T>::unpack(r.a, a);
+  Vec<T>::unpack(r.b, b);
 #pragma unroll
-    for (int j = 0; j < N; ++j) a[j] = b[j] = 0.f;
-  } else if (p.rope) {
-    const float4* cs = reinterpret_cast<const float4*>(p.rope + int64_t(pos) * (p.head_dim / 2) + c * N);
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      const float4 w = __ldg(cs + j);
-      turn(a[2 * j], b[2 * j], make_float2(w.x, w.y));
-      turn(a[2 * j + 1], b[2 * j + 1], make_float2(w.z, w.w));
-    }
-  }
+  for (int j = 0; j < N / 2; ++j) turn2(a[j], b[j], tab[j * lanes + c]);
+  return Raw{Vec<T>::pack(a), Vec<T>::pack(b)};
 }
 
-// Row `h` of token t of q, rotated to q_out (dense [total_new][H_q][d]).
-template <typename T>
-__device__ __forceinline__ void q_row(const AppendParams& p, const Tok& k, int t, int h, int c) {
+// Rows of the tokens t0 .. t0 + n_tok - 1 of a block: K heads (kKV), V heads
+// (kKV) and query heads of each token in turn, a group of d/2 / (16 / sizeof(T))
+// lanes a row. What a row holds does not depend on where it goes, so the first
+// kAhead rows of every group are requested before their tokens are resolved
+// (a warp a token) and arrive under that chain of dependent loads.
+constexpr int kAhead = 3;
+
+template <typename T, bool kKV>
+__device__ __forceinline__ void store_rows(const AppendParams& p, Tok* toks, float4* tab, int t0, int n_tok) {
   constexpr int N = Vec<T>::kN;
   const int half = p.head_dim / 2;
-  float a[N], b[N];
-  const uint8_t* src = p.q + int64_t(t) * p.q_stride + (int64_t(h) * p.head_dim + c * N) * sizeof(T);
-  Vec<T>::load(src, a);
-  Vec<T>::load(src + half * sizeof(T), b);
-  rotate_row<T>(p, k.pos, c, a, b);
-  uint8_t* dst = p.q_out + ((int64_t(t) * p.num_q_heads + h) * p.head_dim + c * N) * sizeof(T);
-  Vec<T>::store(dst, a);
-  Vec<T>::store(dst + half * sizeof(T), b);
-}
-
-}  // namespace
-
-// A block stores tokens_per_block tokens: their descriptors are resolved once
-// into shared memory, then groups of d/2 / (16 / sizeof(T)) lanes take a row
-// (K heads, V heads, query heads of each token in turn).
-template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
-  constexpr int N = Vec<T>::kN;
-  __shared__ Tok toks[kMaxTokensPerBlock];
-  const int t0 = blockIdx.x * p.tokens_per_block;
-  if (threadIdx.x < p.tokens_per_block) toks[threadIdx.x] = token_of(p, t0 + threadIdx.x, true);
-  __syncthreads();
-  const int half = p.head_dim / 2;
+  const int half_bytes = half * int(sizeof(T));
   const int lanes = half / N;                      // lanes of one row
   const int c = threadIdx.x % lanes;
   const int groups = kAppendThreads / lanes;
   const int H = p.num_kv_heads;
-  const int rows = 2 * H + (p.q ? p.num_q_heads : 0);
-  const int64_t row_bytes = int64_t(p.head_dim) * sizeof(T);
-  bool over = false;
-  for (int x = threadIdx.x / lanes; x < rows * p.tokens_per_block; x += groups) {
-    const int n = x / rows, r = x % rows;
-    const Tok k = toks[n];
-    const int t = t0 + n;
-    if (!k.live) continue;
-    if (r >= 2 * H) {
-      q_row<T>(p, k, t, r - 2 * H, c);
-      continue;
+  const int kv = kKV ? 2 * H : 0;
+  const int rows = kv + p.num_q_heads;             // num_q_heads is 0 without queries
+  const int row_bytes = 2 * half_bytes;
+  n_tok = min(n_tok, p.seqs.total_new - t0);
+  // (token, row) of this group's next row to load and next row to store; they
+  // advance by `groups` rows without a division
+  struct At {
+    int n, r;
+  };
+  auto advance = [&](At& a) {
+    a.r += groups;
+    while (a.r >= rows) { a.r -= rows; ++a.n; }
+  };
+  const int x0 = threadIdx.x / lanes;
+  At ld = {x0 / rows, x0 % rows}, st = ld;
+  Raw raw[kAhead];
+  auto load = [&](Raw& w) {
+    if (ld.n < n_tok) {
+      const int64_t t = t0 + ld.n;
+      const uint8_t* at = ld.r >= kv ? p.q + t * p.q_stride + int64_t(ld.r - kv) * row_bytes
+                          : ld.r < H ? p.k + t * p.k_stride + int64_t(ld.r) * row_bytes
+                                     : p.v + t * p.v_stride + int64_t(ld.r - H) * row_bytes;
+      w = load_raw(at + c * 16, half_bytes);
     }
-    if (k.page < 0) continue;
-    const bool is_k = r < H;
-    const int h = is_k ? r : r - H;
-    float a[N], b[N];
-    const uint8_t* src = (is_k ? p.k + int64_t(t) * p.k_stride : p.v + int64_t(t) * p.v_stride) + h * row_bytes +
-                         c * N * int(sizeof(T));
-    Vec<T>::load(src, a);
-    Vec<T>::load(src + half * sizeof(T), b);
-    if (is_k || k.pos < 0) rotate_row<T>(p, k.pos, c, a, b);
-    uint8_t* dst = (is_k ? p.pool_k : p.pool_v) +
-                   (((int64_t(p.layer) * p.num_pages + k.page) * H + h) * kPage + k.slot) * row_bytes +
-                   c * N * int(sizeof(T));
-    if (sizeof(T) == 2 && !is_k) {
-      store_f16(dst, a, over);
-      store_f16(dst + half * sizeof(T), b, over);
-    } else {
-      Vec<T>::store(dst, a);
-      Vec<T>::store(dst + half * sizeof(T), b);
+    advance(ld);
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) load(raw[j]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < n_tok) {
+    const Tok k = token_of(p, t0 + warp, lane, kKV);
+    if (lane == 0) toks[warp] = k;
+    if (p.rope && k.pos >= 0) {
+      const float4* row = reinterpret_cast<const float4*>(p.rope + int64_t(k.pos) * half);
+      for (int f = lane; f < half / 2; f += 32) tab[warp * (half / 2) + tab_at<N>(f, lanes)] = tab_vec(row + f);
     }
   }
+  __syncthreads();
+  bool over = false;
+  while (st.n < n_tok) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (st.n < n_tok) {
+        const int n = st.n, r = st.r;
+        const Tok& k = toks[n];
+        const int pos = k.pos;
+        const bool is_v = kKV && r >= H && r < kv;
+        uint8_t* dst = nullptr;
+        if (r >= kv) {
+          if (k.live) dst = p.q_out + (int64_t(t0 + n) * p.num_q_heads + (r - kv)) * row_bytes;
+        } else if (k.page >= 0) {
+          dst = (is_v ? p.pool_v : p.pool_k) +
+                (((int64_t(p.layer) * p.num_pages + k.page) * H + (is_v ? r - H : r)) * kPage + k.slot) * row_bytes;
+        }
+        if (dst) {
+          Raw w = is_v && pos >= 0 ? raw[j] : turn_raw<T>(p.rope ? tab + n * (half / 2) : nullptr, pos, c, lanes, raw[j]);
+          if (sizeof(T) == 2 && is_v) {   // V of a bf16 cache is stored as fp16 (saturated, reported)
+            uint32_t range = 0;
+            w.a = bf16x8_to_f16x8(w.a, range);
+            w.b = bf16x8_to_f16x8(w.b, range);
+            over = over || range_exceeded(range);
+          }
+          *reinterpret_cast<uint4*>(dst + c * 16) = w.a;
+          *reinterpret_cast<uint4*>(dst + half_bytes + c * 16) = w.b;
+        }
+        load(raw[j]);
+      }
+      advance(st);
+    }
+  }
+  if (over && p.err) atomicOr(p.err, kDevErrRange);
+}
+
+}  // namespace
+
+// A block stores tokens_per_block tokens.
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+  __shared__ Tok toks[kMaxTokensPerBlock];
+  __shared__ float4 tab[kMaxTokensPerBlock * 32];
+  const int t0 = blockIdx.x * p.tokens_per_block;
+  store_rows<T, true>(p, toks, tab, t0, p.tokens_per_block);
   // slots behind a sequence's last token in a page this call began
-  for (int n = 0; n < p.tokens_per_block; ++n) {
+  const int H = p.num_kv_heads;
+  const int row_bytes = p.head_dim * int(sizeof(T));
+  for (int n = 0; n < min(p.tokens_per_block, p.seqs.total_new - t0); ++n) {
     const Tok k = toks[n];
     if (k.page < 0 || k.tail == 0) continue;
-    const int vecs = int(k.tail * row_bytes / 16);
+    const int vecs = k.tail * row_bytes / 16;
     for (int x = threadIdx.x; x < 2 * H * vecs; x += kAppendThreads) {
       const int h = x / vecs % H;
       uint8_t* base = (x / vecs < H ? p.pool_k : p.pool_v) +
@@ -239,140 +316,539 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
       reinterpret_cast<uint4*>(base)[x % vecs] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  if (over && p.err) atomicOr(p.err, kDevErrRange);
 }
 
-// 8-bit pool. A warp owns one (page the call touches, KV head) of K or of V:
-// the block scale needs the largest magnitude of all its new rows, and a scale
-// that grows has to bring the page's held codes along, so the page block is
-// the unit that one warp can settle alone, with no atomics and no second pass.
-// The unit's pages are found without a prefix kernel: sequence s owns the unit
-// numbers from tok_off[s] / 16 + 2 s on, which leaves room for every page that
-// its n tokens can touch ((n + 14) / 16 + 1 at most); units past a sequence's
-// last page have nothing to do. Lane (r, c) = (lane / 8, lane % 8) holds
-// columns 8c.. and 64 + 8c.. of rows r, r + 4, r + 8, r + 12.
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const AppendParams p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = lane & 7, sub = lane >> 3;
-  const int H = p.num_kv_heads;
-  if (int(blockIdx.x) >= p.kv_blocks) {
-    // the queries: a group of 8 lanes per row
-    __shared__ Tok toks[kMaxTokensPerBlock];
-    const int t0 = (int(blockIdx.x) - p.kv_blocks) * p.tokens_per_block;
-    if (threadIdx.x < p.tokens_per_block) toks[threadIdx.x] = token_of(p, t0 + threadIdx.x, false);
-    __syncthreads();
-    for (int x = threadIdx.x >> 3; x < p.num_q_heads * p.tokens_per_block; x += kAppendThreads / 8) {
-      const int n = x / p.num_q_heads;
-      if (toks[n].live) q_row<__nv_bfloat16>(p, toks[n], t0 + n, x % p.num_q_heads, c);
-    }
-    return;
-  }
-  const int64_t task = int64_t(blockIdx.x) * (kAppendThreads / 32) + warp;
-  const int u = int(task / (2 * H));
-  const int r = int(task % (2 * H));
-  const bool is_k = r < H;
-  const int h = is_k ? r : r - H;
-  // last sequence whose first unit is at or before u
-  int lo = 0, hi = p.seqs.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.seqs.tok_off + mid) / kPage + 2 * mid <= u) lo = mid; else hi = mid - 1;
-  }
-  const Seq q = load_seq(p.seqs, lo);
+// 8-bit pool. A warp settles one (page the call touches, KV head) of K or of V
+// at a time: the block scale needs the largest magnitude of all its new rows,
+// and a scale that grows has to bring the page's held codes along, so the page
+// block is the unit that one warp can settle alone, with no atomics. The rows
+// stay in registers as they were read and are turned twice, for the maximum and
+// for the codes: kept as fp32 they would take 64 registers a lane, and the
+// kernel lives on warps in flight. The pages are found without a prefix kernel:
+// sequence s owns the unit numbers from tok_off[s] / 16 + 2 s on, which leaves
+// room for every page that its n tokens can touch ((n + 14) / 16 + 1 at most);
+// units past a sequence's last page have nothing to do. A block resolves
+// units_per_block units at once, a warp each (resolved by every warp for
+// itself, the chain of about ten dependent loads took longer than the rows),
+// and walks their page blocks with the unit's table rows in shared memory.
+// Lane (r, c) = (lane / 8, lane % 8) holds columns 8c.. and 64 + 8c.. of rows
+// r, r + 4, r + 8, r + 12.
+namespace {
+
+struct Unit {
+  int64_t page;        // -1: nothing to do
+  int32_t s0, s1;      // new slots
+  int32_t t0;          // row of k and v that slot 0 would have
+  int32_t pos;         // rotary position that slot 0 would have
+};
+
+__device__ __forceinline__ Unit unit_of(const AppendParams& p, int u, int lane) {
+  Unit x;
+  x.page = -1; x.s0 = x.s1 = x.t0 = x.pos = 0;
+  const int s = last_at_or_before(p.seqs.n_seqs, u, lane,
+                                  [&](int i) { return __ldg(p.seqs.tok_off + i) / kPage + 2 * i; });
+  const Seq q = load_seq(p.seqs, s);
+  const bool report = lane == 0 && p.err;
   if (!q.ok) {
-    if (lane == 0 && p.err) atomicOr(p.err, kDevErrGeometry);
-    return;
+    if (report) atomicOr(p.err, kDevErrGeometry);
+    return x;
   }
-  const int a = q.start / kPage + (u - (q.t0 / kPage + 2 * lo));     // page of the sequence
-  if (q.n == 0 || a < 0 || a > (q.start + q.n - 1) / kPage) return;
-  const int s0 = max(q.start - a * kPage, 0);                         // slots [s0, s1) are new
-  const int s1 = min(q.start + q.n - a * kPage, kPage);
+  const int a = q.start / kPage + (u - (q.t0 / kPage + 2 * s));     // page of the sequence
+  if (q.n == 0 || a < 0 || a > (q.start + q.n - 1) / kPage) return x;
   const int page = __ldg(p.seqs.page_ids + q.p0 + a);
   if (page < 0 || page >= p.num_pages) {
-    if (lane == 0 && p.err) atomicOr(p.err, kDevErrPage);
-    return;
+    if (report) atomicOr(p.err, kDevErrPage);
+    return x;
   }
-  const int64_t block = (int64_t(p.layer) * p.num_pages + page) * H + h;
-  uint8_t* codes = (is_k ? p.pool_k : p.pool_v) + block * (kPage * kHeadDim);
-  float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
-  float old = s0 > 0 ? *scale_at : 0.f;
+  x.page = page;
+  x.s0 = max(q.start - a * kPage, 0);
+  x.s1 = min(q.start + q.n - a * kPage, kPage);
+  x.t0 = q.t0 + a * kPage - q.start;
+  // positions outside the table are found by range, so a sum past 31 bits may not wrap back into it
+  const int64_t pos = int64_t(q.pos0) + int64_t(a) * kPage;
+  x.pos = int32_t(max(int64_t(-64), min(pos, int64_t(1) << 30)));
+  return x;
+}
 
-  float x[4][16];
-  float amax = 0.f;
-  int err = 0;
+// The block's scale from its new rows' largest magnitude and the scale it has.
+struct Scale {
+  float now, inv, ratio;
+  bool regrow;           // held codes follow, times ratio
+};
+template <bool kIsK>
+__device__ __forceinline__ Scale settle(float amax, float old, int s0, int& err) {
+  const int top = kIsK ? kScaleExpMaxK : kScaleExpMaxV;
+  if (amax > kE4m3Max * pow2f(top)) err |= kDevErrRange;
+  const float need = pow2f(scale_exp(amax, top));
+  if (s0 == 0) old = 0.f;
+  if (!(old >= 0.f && old < INFINITY)) { old = need; err |= kDevErrRange; }   // not a scale: the held codes stay
+  Scale s;
+  s.now = fmaxf(old, need);
+  s.inv = __frcp_rn(s.now);   // exact for the powers of two that this kernel writes
+  s.regrow = s0 > 0 && s.now != old;
+  s.ratio = s.regrow ? __fdiv_rn(old, s.now) : 1.f;
+  return s;
+}
+__device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio) {
+  const float2 a = f16x2_to_f32x2(e4m3x2_to_f16x2(w & 0xffffu)), b = f16x2_to_f32x2(e4m3x2_to_f16x2(w >> 16));
+  return e4m3x4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+}
+
+// Row `slot` of a K block turned by its position (outside the table: zeros).
+__device__ __forceinline__ void turned(const AppendParams& p, const Unit& u, const float4* tab, int slot, int c,
+                                       const Raw& r, float2* x, int& err) {
+  Vec<__nv_bfloat16>::unpack(r.a, x);
+  Vec<__nv_bfloat16>::unpack(r.b, x + 4);
+  if (!p.rope) return;
+  if (u.pos + slot < 0 || u.pos + slot >= p.n_pos) {
+    err |= kDevErrGeometry;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = make_float2(0.f, 0.f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) turn2(x[j], x[4 + j], tab[slot * 32 + j * 8 + c]);
+  }
+}
+
+// inf saturates; nan is stored as 0 (a nan code in V would reach, as 0 * nan,
+// rows whose mask hides it).
+__device__ __forceinline__ void no_nan(float2* x) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (x[j].x != x[j].x) x[j].x = 0.f;
+    if (x[j].y != x[j].y) x[j].y = 0.f;
+  }
+}
+
+template <bool kIsK>
+__device__ __forceinline__ void store_block(const AppendParams& p, const Unit& u, const float4* tab, int h, int lane,
+                                            int& err) {
+  const int c = lane & 7, sub = lane >> 3;
+  const int H = p.num_kv_heads;
+  const uint8_t* src = (kIsK ? p.k : p.v) + int64_t(h) * (kHeadDim * 2) + 16 * c;
+  const int64_t stride = kIsK ? p.k_stride : p.v_stride;
+  const int64_t block = (int64_t(p.layer) * p.num_pages + u.page) * H + h;
+  uint8_t* codes = (kIsK ? p.pool_k : p.pool_v) + block * (kPage * kHeadDim) + 8 * c;
+  float* scale_at = (kIsK ? p.k_scale : p.v_scale) + block;
+  float old = u.s0 > 0 ? *scale_at : 0.f;
+
+  Raw raw[4];
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int slot = 4 * it + sub;
-    const bool have = slot >= s0 && slot < s1;
-    if (have) {
-      const int i = a * kPage + slot;                                 // token of the sequence
-      const int t = q.t0 + i - q.start;
-      const uint8_t* src = (is_k ? p.k + int64_t(t) * p.k_stride : p.v + int64_t(t) * p.v_stride) +
-                           (int64_t(h) * kHeadDim + 8 * c) * 2;
-      Vec<__nv_bfloat16>::load(src, x[it]);
-      Vec<__nv_bfloat16>::load(src + kHeadDim, x[it] + 8);
-      const int64_t pos = int64_t(q.pos0) + i;
-      const bool inside = !p.rope || (pos >= 0 && pos < p.n_pos);
-      if (!inside) err |= kDevErrGeometry;
-      if (is_k || !inside) rotate_row<__nv_bfloat16>(p, inside ? (p.rope ? int(pos) : 0) : -1, c, x[it], x[it] + 8);
+    if (slot >= u.s0 && slot < u.s1) raw[it] = load_raw(src + int64_t(u.t0 + slot) * stride, kHeadDim);
+  }
+  float amax = 0.f;
+  bool odd = false;   // a value is not finite
+  if (kIsK) {
+    float amin = 0.f;
+    const float2 zero = make_float2(0.f, 0.f);
+    float2 sum = zero;                          // of x * 0: nan when an x is not finite
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float m = fabsf(x[it][j]);
-        if (m < INFINITY) {
-          amax = fmaxf(amax, m);
-        } else {
-          // inf saturates; nan is stored as 0 (a nan code in V would reach,
-          // as 0 * nan, rows whose mask hides it). Both are reported.
-          err |= kDevErrRange;
-          if (m != m) x[it][j] = 0.f;
+    for (int it = 0; it < 4; ++it) {
+      const int slot = 4 * it + sub;
+      if (slot >= u.s0 && slot < u.s1) {
+        float2 x[8];
+        turned(p, u, tab, slot, c, raw[it], x, err);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sum = ffma2(x[j], zero, sum);
+          amax = fmax3(amax, x[j].x, x[j].y);
+          amin = fmin3(amin, x[j].x, x[j].y);
         }
+      }
+    }
+    amax = fmaxf(amax, -amin);
+    odd = !(sum.x + sum.y == 0.f);
+  } else {
+    uint32_t big = 0;                           // the largest magnitudes' bits, as bf16 pairs
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int slot = 4 * it + sub;
+      if (slot >= u.s0 && slot < u.s1) {
+        if (p.rope && (u.pos + slot < 0 || u.pos + slot >= p.n_pos)) {
+          err |= kDevErrGeometry;
+          raw[it] = Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        }
+        const uint32_t w[8] = {raw[it].a.x, raw[it].a.y, raw[it].a.z, raw[it].a.w,
+                               raw[it].b.x, raw[it].b.y, raw[it].b.z, raw[it].b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) big = __vmaxu2(big, w[j] & 0x7fff7fffu);
+      }
+    }
+    const uint32_t top = max(big >> 16, big & 0xffffu);
+    odd = top >= 0x7f80u;
+    amax = __uint_as_float(top << 16);
+  }
+  if (__any_sync(0xffffffffu, odd)) {           // rare: the scale follows the finite values
+    if (odd) err |= kDevErrRange;
+    amax = 0.f;
+#pragma unroll 1
+    for (int it = 0; it < 4; ++it) {
+      const int slot = 4 * it + sub;
+      if (slot >= u.s0 && slot < u.s1) {
+        const Raw r = it == 0 ? raw[0] : it == 1 ? raw[1] : it == 2 ? raw[2] : raw[3];
+        float2 x[8];
+        Vec<__nv_bfloat16>::unpack(r.a, x);
+        Vec<__nv_bfloat16>::unpack(r.b, x + 4);
+        if (kIsK) turned(p, u, tab, slot, c, r, x, err);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (fabsf(x[j].x) < INFINITY) amax = fmaxf(amax, fabsf(x[j].x));
+          if (fabsf(x[j].y) < INFINITY) amax = fmaxf(amax, fabsf(x[j].y));
+        }
+      }
+    }
+  }
+  const bool any_odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const Scale sc = settle<kIsK>(amax, old, u.s0, err);
+  const float2 inv2 = make_float2(sc.inv, sc.inv);
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int slot = 4 * it + sub;
+    uint2* at0 = reinterpret_cast<uint2*>(codes + slot * kHeadDim);
+    uint2* at1 = reinterpret_cast<uint2*>(codes + slot * kHeadDim + 64);
+    if (slot >= u.s0 && slot < u.s1) {
+      float2 x[8];
+      if (kIsK) {
+        turned(p, u, tab, slot, c, raw[it], x, err);
+      } else {
+        Vec<__nv_bfloat16>::unpack(raw[it].a, x);
+        Vec<__nv_bfloat16>::unpack(raw[it].b, x + 4);
+      }
+      if (any_odd) no_nan(x);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y0 = fmul2(x[2 * j], inv2), y1 = fmul2(x[2 * j + 1], inv2);
+        w[j] = e4m3x4(y0.x, y0.y, y1.x, y1.y);
+      }
+      *at0 = make_uint2(w[0], w[1]);
+      *at1 = make_uint2(w[2], w[3]);
+    } else if (slot < u.s0) {
+      if (sc.regrow) {
+        uint2 w[2] = {*at0, *at1};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          w[k].x = rescaled(w[k].x, sc.ratio);
+          w[k].y = rescaled(w[k].y, sc.ratio);
+        }
+        *at0 = w[0];
+        *at1 = w[1];
+      }
+    } else if (u.s0 == 0) {
+      *at0 = make_uint2(0u, 0u);
+      *at1 = make_uint2(0u, 0u);
+    }
+  }
+  if (lane == 0 && (u.s0 == 0 || sc.regrow)) *scale_at = sc.now;
+}
+
+}  // namespace
+
+// heads_split blocks share a group of units: block y takes page blocks 8 y ..
+// 8 y + 7, 8 (y + heads_split) .. of each, a warp a block.
+__global__ void __launch_bounds__(kAppendThreads, 2) kv8_append_kernel(const AppendParams p) {
+  __shared__ Tok toks[kMaxTokensPerBlock];
+  __shared__ Unit units[kMaxTokensPerBlock];
+  __shared__ float4 tab[2 * kPage * 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (int(blockIdx.x) >= p.kv_blocks) {
+    store_rows<__nv_bfloat16, false>(p, toks, tab, (int(blockIdx.x) - p.kv_blocks) * p.tokens_per_block,
+                                     p.tokens_per_block);
+    return;
+  }
+  const int u0 = int(blockIdx.x) / p.heads_split * p.units_per_block;
+  const int y = int(blockIdx.x) % p.heads_split;
+  if (warp < p.units_per_block) {
+    const Unit u = unit_of(p, u0 + warp, lane);
+    if (lane == 0) units[warp] = u;
+  }
+  __syncthreads();
+  int err = 0;
+  const int H = p.num_kv_heads;
+  for (int i = 0; i < p.units_per_block; ++i) {
+    const Unit u = units[i];
+    if (u.page < 0) continue;
+    float4* rows = tab + (i & 1) * (kPage * 32);   // the buffer before the last sync's is free
+    if (p.rope) {
+      for (int f = u.s0 * 32 + tid; f < u.s1 * 32; f += kAppendThreads) {
+        const int pos = u.pos + (f >> 5);
+        if (pos >= 0 && pos < p.n_pos)
+          rows[(f & ~31) + tab_at<8>(f & 31, 8)] =
+              tab_vec(reinterpret_cast<const float4*>(p.rope + int64_t(pos) * (kHeadDim / 2)) + (f & 31));
+      }
+    }
+    __syncthreads();
+    for (int r = 8 * y + warp; r < 2 * H; r += 8 * p.heads_split) {
+      if (r < H) store_block<true>(p, u, rows, r, lane, err);
+      else store_block<false>(p, u, rows, r - H, lane, err);
+    }
+  }
+  if (err && p.err) atomicOr(p.err, err);
+}
+
+// Many tokens: the same work with the rows streamed through shared memory. A
+// stage is the 16 slots of 8 page blocks (K heads, then V heads of a unit):
+// one bulk copy per slot and tensor brings a token's neighbouring heads, up to
+// 2 KB, while the warps work on the stage before; a warp turns its block's rows
+// from shared memory twice, so that nothing but a row pair lives in registers
+// and no load's latency is a warp's to wait for. (With the rows in registers,
+// 65,536 tokens took 149 us: 80 registers a lane spill, 128 leave 16 warps.)
+// Lane (r, c) = (lane / 16, lane % 16) holds columns 4c.. and 64 + 4c.. of rows
+// r, r + 2, ...
+namespace {
+
+constexpr int kStreamStages = 2;
+constexpr int kStreamThreads = kAppendThreads + 32;   // 8 warps of page blocks, a producer
+constexpr int kStageBytes = kPage * 8 * kHeadDim * 2;
+constexpr int kStageTab = kPage * 32;                 // table rows, float4
+struct StreamCtrl {
+  uint64_t full[kStreamStages], empty[kStreamStages];
+  Unit units[kMaxTokensPerBlock];
+  int32_t abort;
+};
+constexpr size_t kStreamSmem = kStreamStages * (size_t(kStageBytes) + kStageTab * sizeof(float4)) + sizeof(StreamCtrl) + 64;
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Four values of each half of a row: x[0], x[1] | x[2], x[3].
+__device__ __forceinline__ void row_words(const uint8_t* at, uint32_t* u) {
+  const uint2 a = *reinterpret_cast<const uint2*>(at), b = *reinterpret_cast<const uint2*>(at + kHeadDim);
+  u[0] = a.x; u[1] = a.y; u[2] = b.x; u[3] = b.y;
+}
+
+// kPlain: all 16 slots are new and their positions lie inside the table.
+template <bool kIsK, bool kPlain>
+__device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& u, const uint8_t* rows,
+                                             const float4* tab, int h, int lane, int& err) {
+  const int c = lane & 15, sub = lane >> 4;
+  const int64_t block = (int64_t(p.layer) * p.num_pages + u.page) * p.num_kv_heads + h;
+  uint8_t* codes = (kIsK ? p.pool_k : p.pool_v) + block * (kPage * kHeadDim) + sub * kHeadDim + 4 * c;
+  float* scale_at = (kIsK ? p.k_scale : p.v_scale) + block;
+  const float old = !kPlain && u.s0 > 0 ? *scale_at : 0.f;
+  rows += sub * (8 * kHeadDim * 2) + 8 * c;
+  tab += sub * 32 + c;
+  const bool turning = kIsK && p.rope != nullptr;
+  auto is_new = [&](int i) { return kPlain || (2 * i + sub >= u.s0 && 2 * i + sub < u.s1); };
+  auto outside = [&](int i) {
+    return !kPlain && p.rope && (u.pos + 2 * i + sub < 0 || u.pos + 2 * i + sub >= p.n_pos);
+  };
+  // values of row 2 i + sub, turned; outside the table: zeros
+  auto values = [&](int i, float2* x) {
+    uint32_t w[4];
+    row_words(rows + i * (2 * 8 * kHeadDim * 2), w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+    if (outside(i)) {
+      err |= kDevErrGeometry;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = make_float2(0.f, 0.f);
+    } else if (turning) {
+      turn2(x[0], x[2], tab[i * 64]);
+      turn2(x[1], x[3], tab[i * 64 + 16]);
+    }
+  };
+  float amax = 0.f;
+  bool odd;   // a value is not finite
+  if (kIsK) {
+    float amin = 0.f;
+#pragma unroll(kPlain ? 8 : 1)
+    for (int i = 0; i < kPage / 2; ++i) {
+      if (!is_new(i)) continue;
+      float2 x[4];
+      values(i, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        amax = fmax3_nan(amax, x[j].x, x[j].y);
+        amin = fmin3(amin, x[j].x, x[j].y);
+      }
+    }
+    amax = fmax3_nan(amax, -amin, 0.f);
+    odd = !(amax < INFINITY);
+  } else {
+    uint32_t big = 0;                           // the largest magnitudes' bits, as bf16 pairs
+#pragma unroll(kPlain ? 8 : 1)
+    for (int i = 0; i < kPage / 2; ++i) {
+      if (!is_new(i) || outside(i)) continue;
+      uint32_t w[4];
+      row_words(rows + i * (2 * 8 * kHeadDim * 2), w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) big = __vmaxu2(big, w[j] & 0x7fff7fffu);
+    }
+    const uint32_t top = max(big >> 16, big & 0xffffu);
+    odd = top >= 0x7f80u;
+    amax = __uint_as_float(top << 16);
+  }
+  const bool any_odd = __any_sync(0xffffffffu, odd);
+  if (any_odd) {                                // rare: the scale follows the finite values
+    if (odd) err |= kDevErrRange;
+    amax = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < kPage / 2; ++i) {
+      if (!is_new(i)) continue;
+      float2 x[4];
+      values(i, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (fabsf(x[j].x) < INFINITY) amax = fmaxf(amax, fabsf(x[j].x));
+        if (fabsf(x[j].y) < INFINITY) amax = fmaxf(amax, fabsf(x[j].y));
       }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const int top = is_k ? kScaleExpMaxK : kScaleExpMaxV;
-  if (amax > kE4m3Max * pow2f(top)) err |= kDevErrRange;
-  const float need = pow2f(scale_exp(amax, top));
-  if (!(old >= 0.f && old < INFINITY)) { old = need; err |= kDevErrRange; }   // not a scale: the held codes stay
-  const float now = fmaxf(old, need);
-  const float inv = __frcp_rn(now);   // exact for the powers of two that this kernel writes
-  const bool regrow = s0 > 0 && now != old;
-  const float ratio = regrow ? __fdiv_rn(old, now) : 1.f;
+  const Scale sc = settle<kIsK>(amax, old, kPlain ? 0 : u.s0, err);
+  const float2 inv2 = make_float2(sc.inv, sc.inv);
+#pragma unroll(kPlain ? 8 : 1)
+  for (int i = 0; i < kPage / 2; ++i) {
+    uint32_t* at0 = reinterpret_cast<uint32_t*>(codes + 2 * i * kHeadDim);
+    uint32_t* at1 = at0 + 16;
+    if (is_new(i)) {
+      float2 x[4];
+      values(i, x);
+      if (any_odd) {   // inf saturates, nan becomes 0
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int slot = 4 * it + sub;
-    uint2* at0 = reinterpret_cast<uint2*>(codes + slot * kHeadDim + 8 * c);
-    uint2* at1 = reinterpret_cast<uint2*>(codes + slot * kHeadDim + 64 + 8 * c);
-    if (slot >= s0 && slot < s1) {
-      float* y = x[it];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] *= inv;
-      *at0 = make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
-      *at1 = make_uint2(e4m3x4(y[8], y[9], y[10], y[11]), e4m3x4(y[12], y[13], y[14], y[15]));
-    } else if (slot < s0) {
-      if (regrow) {
-        uint2 w[2] = {*at0, *at1};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t* v = reinterpret_cast<uint32_t*>(&w[k]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float2 f0 = f16x2_to_f32x2(e4m3x2_to_f16x2(v[j] & 0xffffu));
-            const float2 f1 = f16x2_to_f32x2(e4m3x2_to_f16x2(v[j] >> 16));
-            v[j] = e4m3x4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
-          }
+        for (int j = 0; j < 4; ++j) {
+          if (x[j].x != x[j].x) x[j].x = 0.f;
+          if (x[j].y != x[j].y) x[j].y = 0.f;
         }
-        *at0 = w[0];
-        *at1 = w[1];
       }
-    } else if (s0 == 0) {
-      *at0 = make_uint2(0u, 0u);
-      *at1 = make_uint2(0u, 0u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = fmul2(x[j], inv2);
+      *at0 = e4m3x4(x[0].x, x[0].y, x[1].x, x[1].y);
+      *at1 = e4m3x4(x[2].x, x[2].y, x[3].x, x[3].y);
+    } else if (2 * i + sub < u.s0) {
+      if (sc.regrow) {
+        *at0 = rescaled(*at0, sc.ratio);
+        *at1 = rescaled(*at1, sc.ratio);
+      }
+    } else if (u.s0 == 0) {
+      *at0 = 0u;
+      *at1 = 0u;
     }
   }
-  if (lane == 0 && (s0 == 0 || regrow)) *scale_at = now;
+  if (lane == 0 && (kPlain || u.s0 == 0 || sc.regrow)) *scale_at = sc.now;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(const AppendParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((16 - (smem_u32(smem_raw) & 15)) & 15);
+  float4* tabs = reinterpret_cast<float4*>(smem + kStreamStages * kStageBytes);
+  StreamCtrl* ctl = reinterpret_cast<StreamCtrl*>(tabs + kStreamStages * kStageTab);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < kStreamStages; ++s) {
+      mbar_init(&ctl->full[s], 2);     // the copies' bytes and the table rows
+      mbar_init(&ctl->empty[s], 8);
+    }
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp < p.units_per_block) {
+    const Unit u = unit_of(p, int(blockIdx.x) * p.units_per_block + warp, lane);
+    if (lane == 0) ctl->units[warp] = u;
+  }
+  __syncthreads();
+  volatile int* abort_flag = &ctl->abort;
+  const int H = p.num_kv_heads;
+  const int groups = (2 * H + 7) / 8;   // stages of a unit
+  if (warp == 8) {
+    uint32_t n = 0;
+    bool bad = false;
+    for (int i = 0; i < p.units_per_block && !bad; ++i) {
+      const Unit u = ctl->units[i];
+      if (u.page < 0) continue;
+      for (int y = 0; y < groups; ++y, ++n) {
+        const int s = n % kStreamStages;
+        if (n >= uint32_t(kStreamStages) && !mbar_wait(&ctl->empty[s], (n / kStreamStages - 1) & 1, abort_flag)) {
+          bad = true;
+          break;
+        }
+        __syncwarp();
+        const int r0 = 8 * y, r1 = min(r0 + 8, 2 * H);
+        const int nk = max(min(r1, H) - r0, 0), nv = r1 - r0 - nk;    // K heads, then V heads
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->full[s], uint32_t((u.s1 - u.s0) * (r1 - r0) * kHeadDim * 2));
+        __syncwarp();
+        if (lane >= u.s0 && lane < u.s1) {
+          uint8_t* dst = smem + s * kStageBytes + lane * (8 * kHeadDim * 2);
+          const int64_t t = u.t0 + lane;
+          if (nk > 0) bulk_load(dst, p.k + t * p.k_stride + int64_t(r0) * kHeadDim * 2, nk * kHeadDim * 2, &ctl->full[s]);
+          if (nv > 0)
+            bulk_load(dst + nk * kHeadDim * 2, p.v + t * p.v_stride + int64_t(r0 + nk - H) * kHeadDim * 2,
+                      nv * kHeadDim * 2, &ctl->full[s]);
+        }
+        if (p.rope && nk > 0) {
+          float4* rows = tabs + s * kStageTab;
+#pragma unroll 8
+          for (int slot = u.s0; slot < u.s1; ++slot) {
+            const int pos = u.pos + slot;
+            if (pos >= 0 && pos < p.n_pos)
+              rows[slot * 32 + tab_at<4>(lane, 16)] =
+                  tab_vec(reinterpret_cast<const float4*>(p.rope + int64_t(pos) * (kHeadDim / 2)) + lane);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[s]);
+      }
+    }
+    if (bad) {
+      if (lane == 0 && p.err) atomicOr(p.err, kDevErrTimeout);
+      ctl->abort = 1;
+    }
+    // let every copy this warp issued land before the block exits
+    if (lane == 0 && ctl->abort) {
+      int zero = 0;
+      for (uint32_t t = n > kStreamStages ? n - kStreamStages : 0; t < n; ++t)
+        mbar_wait(&ctl->full[t % kStreamStages], (t / kStreamStages) & 1, &zero);
+    }
+    __syncwarp();
+    return;
+  }
+  uint32_t n = 0;
+  int err = 0;
+  for (int i = 0; i < p.units_per_block; ++i) {
+    const Unit u = ctl->units[i];
+    if (u.page < 0) continue;
+    for (int y = 0; y < groups; ++y, ++n) {
+      const int s = n % kStreamStages;
+      if (!mbar_wait(&ctl->full[s], (n / kStreamStages) & 1, abort_flag)) {
+        if (lane == 0 && p.err) atomicOr(p.err, kDevErrTimeout);
+        ctl->abort = 1;
+        return;
+      }
+      const int r = 8 * y + warp;
+      const uint8_t* rows = smem + s * kStageBytes + warp * (kHeadDim * 2);
+      const float4* tab = tabs + s * kStageTab;
+      const bool plain = u.s0 == 0 && u.s1 == kPage && (!p.rope || (u.pos >= 0 && u.pos + kPage <= p.n_pos));
+      if (r < H) {
+        if (plain) stream_block<true, true>(p, u, rows, tab, r, lane, err);
+        else stream_block<true, false>(p, u, rows, tab, r, lane, err);
+      } else if (r < 2 * H) {
+        if (plain) stream_block<false, true>(p, u, rows, tab, r - H, lane, err);
+        else stream_block<false, false>(p, u, rows, tab, r - H, lane, err);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->empty[s]);
+    }
+  }
   if (err && p.err) atomicOr(p.err, err);
+}
+
+// Queries alone, beside the streamed cache blocks of a call with many tokens.
+__global__ void __launch_bounds__(kAppendThreads) rope_q_kernel(const AppendParams p) {
+  __shared__ Tok toks[kMaxTokensPerBlock];
+  __shared__ float4 tab[kMaxTokensPerBlock * 32];
+  store_rows<__nv_bfloat16, false>(p, toks, tab, int(blockIdx.x) * p.tokens_per_block, p.tokens_per_block);
 }
 
 // (cos, sin) of position p and pair i: the angle p * base^(-2 i / d), in fp64,
@@ -395,6 +871,15 @@ cudaError_t launch_kv_append(const AppendParams& p, int is_f32, int grid, cudaSt
 }
 cudaError_t launch_kv8_append(const AppendParams& p, int grid, cudaStream_t stream) {
   return launch_plain(kv8_append_kernel, dim3(grid), dim3(kAppendThreads), 0, stream, p);
+}
+cudaError_t launch_kv8_append_stream(const AppendParams& p, int grid, cudaStream_t stream) {
+  static SmemAttr attr;
+  const cudaError_t e = ensure_smem_attr(kv8_append_stream_kernel, attr, kStreamSmem);
+  if (e != cudaSuccess) return e;
+  return launch_plain(kv8_append_stream_kernel, dim3(grid), dim3(kStreamThreads), kStreamSmem, stream, p);
+}
+cudaError_t launch_rope_q(const AppendParams& p, int grid, cudaStream_t stream) {
+  return launch_plain(rope_q_kernel, dim3(grid), dim3(kAppendThreads), 0, stream, p);
 }
 cudaError_t launch_rope_cos_sin(double base, int head_dim, int n_pos, float2* table, cudaStream_t stream) {
   const int64_t n = int64_t(n_pos) * (head_dim / 2);

@@ -20,7 +20,7 @@ RAG_BF16, RAG_F32 = 0, 1
 PAGE_SIZE = 16
 KERNEL_KINDS = ("pool_write", "attn", "combine", "impact", "topk", "simt_attn", "simt_impact", "rc_plan", "rc_copy",
                 "rc_gemm", "rope_table", "kv_decode", "attn_dec", "kv_append", "kv8_append", "rope_cos_sin",
-                "kv8_attn", "kv8_combine", "kv8_split_q", "kv8_attn_dec")
+                "kv8_attn", "kv8_combine", "kv8_split_q", "kv8_attn_dec", "rope_q")
 
 STATUS = {
     0: "ok", 1: "invalid argument", 2: "inconsistent shape", 3: "page id outside the pool",

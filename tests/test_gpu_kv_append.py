@@ -384,3 +384,55 @@ def test_offsets_past_32_bits():
     ref = k[:16].float().permute(1, 0, 2)
     assert ((x - ref).abs() <= ref.abs() / 16 + pool.k_scale[0, P - 1][:, None, None] * 2.0 ** -10).all()
     assert not pool.k[0, :100].view(torch.uint8).any()
+
+
+# calls with many tokens stream their rows through shared memory
+@pytest.mark.parametrize("fused,pad,rope", [(False, 0, True), (True, 5, True), (False, 0, False)])
+@pytest.mark.parametrize("H,starts,news", [(32, [0, 5, 31, 16], [300, 1, 170, 160]), (3, [7, 0], [3000, 3400]),
+                                           (1, [0], [19000]), (20, [3, 15, 0], [500, 17, 513])])
+def test_streamed_calls(H, starts, news, fused, pad, rope):
+    case = Case("e4m3", starts, news, H=H, G=2, fused=fused, pad=pad, seed=H, n_pos=20000, rope=rope)
+    before = case.state()
+    case.run()
+    check(case, before, case.state(), case.oracle(before))
+    check_q(case)
+    assert int(case.err.item()) == 0
+
+
+def test_streamed_calls_give_the_bits_of_small_ones():
+    """The same tokens in one call and page by page: the same codes, scales and
+    queries, whatever the kernel (a page's rows are all in one call either way)."""
+    a, b = (Case("e4m3", [0, 8], [320, 312], H=32, G=1, seed=3) for _ in range(2))
+    a.run()
+    t = 0
+    for pages, start, n, pos0 in b.seqs:
+        at = start
+        while at < start + n:
+            m = min(16 - at % 16, start + n - at)
+            s = sp.Append([0, m], [at], [0, len(pages)], pages, pos0=[pos0])
+            sp.rag_kv8_append(b.pool, 1, s, b.k[t:t + m], b.v[t:t + m], rope=b.rope, q=b.q[t:t + m],
+                              q_out=b.q_out[t:t + m])
+            at, t = at + m, t + m
+    for x, y in zip(a.state(), b.state()):
+        np.testing.assert_array_equal(x, y)
+    assert torch.equal(a.q_out, b.q_out)
+
+
+def test_streamed_infinities_bad_pages_and_positions():
+    case = Case("e4m3", [0, 4, 0], [400, 300, 300], H=32, G=1, seed=4)
+    tok, start, po, ids, pos0 = case.arrays
+    ids = list(ids)
+    ids[po[0] + 1] = -1
+    case.append_c = sp.Append(tok, start, po, ids, pos0=[pos0[0], pos0[1], 4096 - 20])
+    case.k[3, 0, 7], case.k[5, 1, 0] = float("inf"), float("nan")
+    case.v[402, 31, 1], case.v[402, 30, 2] = float("-inf"), float("nan")
+    before = case.state()
+    case.run()
+    after = case.state()
+    assert int(case.err.item()) == 1 | 2 | 8
+    p0, p1, p2 = (s[0] for s in case.seqs)
+    np.testing.assert_array_equal(after[0][p0[1]], before[0][p0[1]])
+    assert after[0][p0[0], 1, 5, 0] == 0 and np.isfinite(after[0][p0[0]]).all() and np.isfinite(after[2][p0[0]]).all()
+    assert after[1][p1[0], 31, 6, 1] == -448 and after[1][p1[0], 30, 6, 2] == 0
+    assert after[0][p2[1], :, :4].any() and not after[0][p2[1], :, 4:].any() and not after[1][p2[5]].any()
+    assert not case.q_out[720:].any() and case.q_out[719].any()
