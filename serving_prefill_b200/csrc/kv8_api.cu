@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "rag_prefill.h"
 #include "host.cuh"
@@ -68,8 +69,9 @@ static rag_status check_append(AppendParams& p, int elem, int num_layers, int la
   p.n_pos = rope ? n_pos : 0;
   p.layer = layer;
   p.num_q_heads = q ? num_q_heads : 0;
-  // enough blocks to fill the GPU twice before a block takes several tokens
-  p.tokens_per_block = std::max(1, std::min(8, seqs->total_new / (4 * num_sms())));
+  // a power of two, as few as let every block (three an SM) start at once
+  p.tokens_per_block = 1;
+  while (p.tokens_per_block < 8 && seqs->total_new > 3 * p.tokens_per_block * num_sms()) p.tokens_per_block *= 2;
   p.kv_blocks = 0;
   return RAG_OK;
 }
@@ -87,7 +89,7 @@ struct Kv8Plan {
 // is, for one request (alike items), ceil(items / SMs) of them after one
 // another, for several the list-scheduling bound (average load per SM plus one
 // longest item), an item's start and end counted as two tiles.
-static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
+static Kv8Plan plan_kv8_uncached(const rag_batch& b, int num_kv_heads, int group, int sms) {
   Kv8Plan pl;
   pl.decode = int64_t(b.max_q) * group <= 16 ? 1 : 0;
   pl.toks_per_block = pl.decode ? 16 / group : kQTiles * (kBM / group);
@@ -115,6 +117,26 @@ static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms
   const int64_t rt_bound = cdiv(b.total_q, pl.toks_per_block) + int64_t(b.num_requests);
   pl.max_items = int64_t(num_kv_heads) * rt_bound * cdiv(tiles_max, best_ts);
   pl.grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, pl.max_items)));
+  return pl;
+}
+
+// The plan reads only these totals and the shape, so the last few are kept per
+// host thread (every layer of a step, every step of a batch has the same).
+static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
+  struct Key {
+    int32_t v[8];
+  };
+  constexpr int kKept = 8;
+  thread_local Key keys[kKept];
+  thread_local Kv8Plan plans[kKept];
+  thread_local int n = 0, next = 0;
+  const Key k = {{b.num_requests, b.max_pages, b.max_q, b.total_q, b.num_page_refs, num_kv_heads, group, sms}};
+  for (int i = 0; i < n; ++i)
+    if (std::memcmp(&keys[i], &k, sizeof(Key)) == 0) return plans[i];
+  const Kv8Plan pl = plan_kv8_uncached(b, num_kv_heads, group, sms);
+  const int slot = n < kKept ? n++ : (next++ % kKept);
+  keys[slot] = k;
+  plans[slot] = pl;
   return pl;
 }
 

@@ -34,7 +34,7 @@ constexpr int kAppendThreads = 256;
 constexpr int kMaxTokensPerBlock = 8;
 
 struct Tok {
-  int64_t page;      // -1: not stored
+  int64_t off;       // byte of its slot in head 0's page block of the pool; -1: not stored
   int32_t slot;
   int32_t pos;       // row of the table; -1: outside it (the row becomes zeros)
   int32_t tail;      // slots behind this token to zero
@@ -78,9 +78,9 @@ __device__ __forceinline__ Seq load_seq(const AppendSeqs& a, int s) {
 }
 
 // Resolve token t (whole warp; lane 0 reports).
-__device__ __forceinline__ Tok token_of(const AppendParams& p, int t, int lane, bool report) {
+__device__ __forceinline__ Tok token_of(const AppendParams& p, int t, int row_bytes, int lane, bool report) {
   Tok k;
-  k.page = -1; k.slot = 0; k.pos = -1; k.tail = 0; k.live = 0;
+  k.off = -1; k.slot = 0; k.pos = -1; k.tail = 0; k.live = 0;
   report = report && lane == 0 && p.err;
   const int end = __ldg(p.seqs.tok_off + p.seqs.n_seqs);
   const int s = last_at_or_before(p.seqs.n_seqs, t, lane, [&](int i) { return __ldg(p.seqs.tok_off + i); });
@@ -106,8 +106,8 @@ __device__ __forceinline__ Tok token_of(const AppendParams& p, int t, int lane, 
     if (report) atomicOr(p.err, kDevErrPage);
     return k;
   }
-  k.page = page;
   k.slot = i % kPage;
+  k.off = ((int64_t(p.layer) * p.num_pages + page) * p.num_kv_heads * kPage + k.slot) * row_bytes;
   if (at == q.n - 1 && i - k.slot >= q.start) k.tail = kPage - 1 - k.slot;
   return k;
 }
@@ -190,104 +190,101 @@ template <> struct Vec<float> {
   }
 };
 
-// Row turned by the table row at tab (null: as it is); pos < 0: zeros.
-template <typename T>
-__device__ __forceinline__ Raw turn_raw(const float4* tab, int pos, int c, int lanes, const Raw& r) {
-  constexpr int N = Vec<T>::kN;
-  if (pos < 0) return Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (!tab) return r;
-  float2 a[N / 2], b[N / 2];
-  Vec<T>::unpack(r.a, a);
-  Vec<T>::unpack(r.b, b);
-#pragma unroll
-  for (int j = 0; j < N / 2; ++j) turn2(a[j], b[j], tab[j * lanes + c]);
-  return Raw{Vec<T>::pack(a), Vec<T>::pack(b)};
-}
-
-// Rows of the tokens t0 .. t0 + n_tok - 1 of a block: K heads (kKV), V heads
-// (kKV) and query heads of each token in turn, a group of d/2 / (16 / sizeof(T))
-// lanes a row. What a row holds does not depend on where it goes, so the first
-// kAhead rows of every group are requested before their tokens are resolved
-// (a warp a token) and arrive under that chain of dependent loads.
+// Rows of the tokens t0 .. t0 + n_tok - 1 of a block of tpb tokens (a power of
+// two): K heads (kKV), V heads (kKV) and query heads, a group of d/2 / (16 /
+// sizeof(T)) lanes a row. A group keeps to one token, so that its table vectors
+// are read once and stay in registers. What a row holds does not depend on
+// where it goes: the first kAhead rows of every group are requested before the
+// tokens are resolved (a warp a token) and arrive under that chain of
+// dependent loads.
 constexpr int kAhead = 3;
 
-template <typename T, bool kKV>
-__device__ __forceinline__ void store_rows(const AppendParams& p, Tok* toks, float4* tab, int t0, int n_tok) {
+template <typename T, int kDim, bool kKV>
+__device__ __forceinline__ void store_rows(const AppendParams& p, Tok* toks, float4* tab, int t0, int tpb) {
   constexpr int N = Vec<T>::kN;
-  const int half = p.head_dim / 2;
-  const int half_bytes = half * int(sizeof(T));
-  const int lanes = half / N;                      // lanes of one row
-  const int c = threadIdx.x % lanes;
-  const int groups = kAppendThreads / lanes;
+  constexpr int kHalf = kDim / 2, kHalfBytes = kHalf * int(sizeof(T)), kRowBytes = 2 * kHalfBytes;
+  constexpr int kLanes = kHalf / N;                // lanes of one row
+  constexpr int kGroups = kAppendThreads / kLanes;
+  const int c = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
   const int H = p.num_kv_heads;
   const int kv = kKV ? 2 * H : 0;
   const int rows = kv + p.num_q_heads;             // num_q_heads is 0 without queries
-  const int row_bytes = 2 * half_bytes;
-  n_tok = min(n_tok, p.seqs.total_new - t0);
-  // (token, row) of this group's next row to load and next row to store; they
-  // advance by `groups` rows without a division
-  struct At {
-    int n, r;
-  };
-  auto advance = [&](At& a) {
-    a.r += groups;
-    while (a.r >= rows) { a.r -= rows; ++a.n; }
-  };
-  const int x0 = threadIdx.x / lanes;
-  At ld = {x0 / rows, x0 % rows}, st = ld;
+  const int n_tok = min(tpb, p.seqs.total_new - t0);
+  const int gpt = kGroups / tpb;                   // groups of a token
+  const int n = grp / gpt, r0 = grp % gpt;
+  const int64_t t = t0 + n;
+  const bool mine = n < n_tok;
   Raw raw[kAhead];
-  auto load = [&](Raw& w) {
-    if (ld.n < n_tok) {
-      const int64_t t = t0 + ld.n;
-      const uint8_t* at = ld.r >= kv ? p.q + t * p.q_stride + int64_t(ld.r - kv) * row_bytes
-                          : ld.r < H ? p.k + t * p.k_stride + int64_t(ld.r) * row_bytes
-                                     : p.v + t * p.v_stride + int64_t(ld.r - H) * row_bytes;
-      w = load_raw(at + c * 16, half_bytes);
+  auto load = [&](Raw& w, int row) {
+    if (!mine || row >= rows) return;
+    const uint8_t* base = p.q;
+    int64_t stride = p.q_stride;
+    int r = row - kv;
+    if (kKV && r < 0) {
+      const bool is_k = row < H;
+      base = is_k ? p.k : p.v;
+      stride = is_k ? p.k_stride : p.v_stride;
+      r = is_k ? row : row - H;
     }
-    advance(ld);
+    w = load_raw(base + t * stride + uint32_t(r * kRowBytes + c * 16), kHalfBytes);
   };
 #pragma unroll
-  for (int j = 0; j < kAhead; ++j) load(raw[j]);
+  for (int j = 0; j < kAhead; ++j) load(raw[j], r0 + j * gpt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp < n_tok) {
-    const Tok k = token_of(p, t0 + warp, lane, kKV);
+    const Tok k = token_of(p, t0 + warp, kRowBytes, lane, kKV);
     if (lane == 0) toks[warp] = k;
     if (p.rope && k.pos >= 0) {
-      const float4* row = reinterpret_cast<const float4*>(p.rope + int64_t(k.pos) * half);
-      for (int f = lane; f < half / 2; f += 32) tab[warp * (half / 2) + tab_at<N>(f, lanes)] = tab_vec(row + f);
+      const float4* row = reinterpret_cast<const float4*>(p.rope + int64_t(k.pos) * kHalf);
+      if (lane < kHalf / 2) tab[warp * (kHalf / 2) + tab_at<N>(lane, kLanes)] = tab_vec(row + lane);
     }
   }
   __syncthreads();
+  if (!mine) return;
+  const Tok k = toks[n];
+  const bool zero = k.pos < 0, turning = p.rope != nullptr && !zero;
+  float4 cs[N / 2];
+  if (turning) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) cs[j] = tab[n * (kHalf / 2) + j * kLanes + c];
+  }
   bool over = false;
-  while (st.n < n_tok) {
+  for (int row0 = r0; row0 < rows; row0 += kAhead * gpt) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (st.n < n_tok) {
-        const int n = st.n, r = st.r;
-        const Tok& k = toks[n];
-        const int pos = k.pos;
-        const bool is_v = kKV && r >= H && r < kv;
-        uint8_t* dst = nullptr;
-        if (r >= kv) {
-          if (k.live) dst = p.q_out + (int64_t(t0 + n) * p.num_q_heads + (r - kv)) * row_bytes;
-        } else if (k.page >= 0) {
-          dst = (is_v ? p.pool_v : p.pool_k) +
-                (((int64_t(p.layer) * p.num_pages + k.page) * H + (is_v ? r - H : r)) * kPage + k.slot) * row_bytes;
-        }
-        if (dst) {
-          Raw w = is_v && pos >= 0 ? raw[j] : turn_raw<T>(p.rope ? tab + n * (half / 2) : nullptr, pos, c, lanes, raw[j]);
-          if (sizeof(T) == 2 && is_v) {   // V of a bf16 cache is stored as fp16 (saturated, reported)
-            uint32_t range = 0;
-            w.a = bf16x8_to_f16x8(w.a, range);
-            w.b = bf16x8_to_f16x8(w.b, range);
-            over = over || range_exceeded(range);
-          }
-          *reinterpret_cast<uint4*>(dst + c * 16) = w.a;
-          *reinterpret_cast<uint4*>(dst + half_bytes + c * 16) = w.b;
-        }
-        load(raw[j]);
+      const int row = row0 + j * gpt;
+      if (row >= rows) break;
+      int r = row - kv;
+      bool store = k.live, is_v = false;
+      uint8_t* dst = p.q_out + t * (p.num_q_heads * kRowBytes) + uint32_t(r * kRowBytes);
+      if (kKV && r < 0) {
+        is_v = row >= H;
+        r = is_v ? row - H : row;
+        store = k.off >= 0;
+        dst = (is_v ? p.pool_v : p.pool_k) + k.off + uint32_t(r * (kPage * kRowBytes));
       }
-      advance(st);
+      Raw w = raw[j];
+      load(raw[j], row + kAhead * gpt);
+      if (!store) continue;
+      if (zero) {
+        w = Raw{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      } else if (turning && !is_v) {
+        float2 a[N / 2], b[N / 2];
+        Vec<T>::unpack(w.a, a);
+        Vec<T>::unpack(w.b, b);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) turn2(a[i], b[i], cs[i]);
+        w.a = Vec<T>::pack(a);
+        w.b = Vec<T>::pack(b);
+      }
+      if (sizeof(T) == 2 && is_v) {   // V of a bf16 cache is stored as fp16 (saturated, reported)
+        uint32_t range = 0;
+        w.a = bf16x8_to_f16x8(w.a, range);
+        w.b = bf16x8_to_f16x8(w.b, range);
+        over = over || range_exceeded(range);
+      }
+      *reinterpret_cast<uint4*>(dst + c * 16) = w.a;
+      *reinterpret_cast<uint4*>(dst + kHalfBytes + c * 16) = w.b;
     }
   }
   if (over && p.err) atomicOr(p.err, kDevErrRange);
@@ -296,23 +293,22 @@ __device__ __forceinline__ void store_rows(const AppendParams& p, Tok* toks, flo
 }  // namespace
 
 // A block stores tokens_per_block tokens.
-template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+template <typename T, int kDim>
+__global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const AppendParams p) {
   __shared__ Tok toks[kMaxTokensPerBlock];
   __shared__ float4 tab[kMaxTokensPerBlock * 32];
   const int t0 = blockIdx.x * p.tokens_per_block;
-  store_rows<T, true>(p, toks, tab, t0, p.tokens_per_block);
+  store_rows<T, kDim, true>(p, toks, tab, t0, p.tokens_per_block);
   // slots behind a sequence's last token in a page this call began
   const int H = p.num_kv_heads;
-  const int row_bytes = p.head_dim * int(sizeof(T));
+  constexpr int row_bytes = kDim * int(sizeof(T));
   for (int n = 0; n < min(p.tokens_per_block, p.seqs.total_new - t0); ++n) {
     const Tok k = toks[n];
-    if (k.page < 0 || k.tail == 0) continue;
+    if (k.off < 0 || k.tail == 0) continue;
     const int vecs = k.tail * row_bytes / 16;
     for (int x = threadIdx.x; x < 2 * H * vecs; x += kAppendThreads) {
       const int h = x / vecs % H;
-      uint8_t* base = (x / vecs < H ? p.pool_k : p.pool_v) +
-                      (((int64_t(p.layer) * p.num_pages + k.page) * H + h) * kPage + k.slot + 1) * row_bytes;
+      uint8_t* base = (x / vecs < H ? p.pool_k : p.pool_v) + k.off + (int64_t(h) * kPage + 1) * row_bytes;
       reinterpret_cast<uint4*>(base)[x % vecs] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -556,7 +552,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv8_append_kernel(const App
   __shared__ float4 tab[2 * kPage * 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (int(blockIdx.x) >= p.kv_blocks) {
-    store_rows<__nv_bfloat16, false>(p, toks, tab, (int(blockIdx.x) - p.kv_blocks) * p.tokens_per_block,
+    store_rows<__nv_bfloat16, kHeadDim, false>(p, toks, tab, (int(blockIdx.x) - p.kv_blocks) * p.tokens_per_block,
                                      p.tokens_per_block);
     return;
   }
@@ -593,21 +589,25 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv8_append_kernel(const App
 // Many tokens: the same work with the rows streamed through shared memory. A
 // stage is the 16 slots of 8 page blocks (K heads, then V heads of a unit):
 // one bulk copy per slot and tensor brings a token's neighbouring heads, up to
-// 2 KB, while the warps work on the stage before; a warp turns its block's rows
-// from shared memory twice, so that nothing but a row pair lives in registers
-// and no load's latency is a warp's to wait for. (With the rows in registers,
-// 65,536 tokens took 149 us: 80 registers a lane spill, 128 leave 16 warps.)
-// Lane (r, c) = (lane / 16, lane % 16) holds columns 4c.. and 64 + 4c.. of rows
-// r, r + 2, ...
+// 2 KB, while the warps work on the stage before; two warps turn a block's rows
+// from shared memory twice, for the maximum (which they exchange) and for the
+// codes, so that little lives in registers and no load's latency is a warp's
+// to wait for. (With the rows in registers, 65,536 tokens took 149 us: 80
+// registers a lane spill, 128 leave 16 warps an SM. One warp a block: 114 us,
+// 1.4 instructions a cycle from 17 warps.)
+// Lane (r, c) = (lane / 16, lane % 16) of half-block b holds columns 4c.. and
+// 64 + 4c.. of rows 8 b + r, 8 b + r + 2, ...
 namespace {
 
 constexpr int kStreamStages = 2;
-constexpr int kStreamThreads = kAppendThreads + 32;   // 8 warps of page blocks, a producer
+constexpr int kStreamThreads = 16 * 32 + 32;           // two warps a page block, a producer
 constexpr int kStageBytes = kPage * 8 * kHeadDim * 2;
 constexpr int kStageTab = kPage * 32;                 // table rows, float4
 struct StreamCtrl {
   uint64_t full[kStreamStages], empty[kStreamStages];
   Unit units[kMaxTokensPerBlock];
+  float big[2][16];       // largest magnitudes of the half-blocks, by stage parity
+  float big_finite[16];
   int32_t abort;
 };
 constexpr size_t kStreamSmem = kStreamStages * (size_t(kStageBytes) + kStageTab * sizeof(float4)) + sizeof(StreamCtrl) + 64;
@@ -628,8 +628,10 @@ __device__ __forceinline__ void row_words(const uint8_t* at, uint32_t* u) {
 // kPlain: all 16 slots are new and their positions lie inside the table.
 template <bool kIsK, bool kPlain>
 __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& u, const uint8_t* rows,
-                                             const float4* tab, int h, int lane, int& err) {
-  const int c = lane & 15, sub = lane >> 4;
+                                             const float4* tab, int h, int warp, int lane, float* big,
+                                             float* big_finite, int& err) {
+  const int c = lane & 15, sub = (warp & 1) * 8 + (lane >> 4);   // first row
+  constexpr int kIts = 4;                                        // rows sub, sub + 2, sub + 4, sub + 6
   const int64_t block = (int64_t(p.layer) * p.num_pages + u.page) * p.num_kv_heads + h;
   uint8_t* codes = (kIsK ? p.pool_k : p.pool_v) + block * (kPage * kHeadDim) + sub * kHeadDim + 4 * c;
   float* scale_at = (kIsK ? p.k_scale : p.v_scale) + block;
@@ -660,8 +662,8 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
   bool odd;   // a value is not finite
   if (kIsK) {
     float amin = 0.f;
-#pragma unroll(kPlain ? 8 : 1)
-    for (int i = 0; i < kPage / 2; ++i) {
+#pragma unroll(kPlain ? kIts : 1)
+    for (int i = 0; i < kIts; ++i) {
       if (!is_new(i)) continue;
       float2 x[4];
       values(i, x);
@@ -675,8 +677,8 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
     odd = !(amax < INFINITY);
   } else {
     uint32_t big = 0;                           // the largest magnitudes' bits, as bf16 pairs
-#pragma unroll(kPlain ? 8 : 1)
-    for (int i = 0; i < kPage / 2; ++i) {
+#pragma unroll(kPlain ? kIts : 1)
+    for (int i = 0; i < kIts; ++i) {
       if (!is_new(i) || outside(i)) continue;
       uint32_t w[4];
       row_words(rows + i * (2 * 8 * kHeadDim * 2), w);
@@ -687,12 +689,21 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
     odd = top >= 0x7f80u;
     amax = __uint_as_float(top << 16);
   }
-  const bool any_odd = __any_sync(0xffffffffu, odd);
+  // both warps' maximum; a value that is not finite makes it infinite
+  auto shared_max = [&](float m, float* at) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) at[warp] = m;
+    named_bar_sync(1 + (warp >> 1), 64);
+    return fmaxf(at[warp & ~1], at[warp | 1]);
+  };
+  if (odd) err |= kDevErrRange;
+  amax = shared_max(odd ? INFINITY : amax, big);
+  const bool any_odd = amax == INFINITY;
   if (any_odd) {                                // rare: the scale follows the finite values
-    if (odd) err |= kDevErrRange;
     amax = 0.f;
 #pragma unroll 1
-    for (int i = 0; i < kPage / 2; ++i) {
+    for (int i = 0; i < kIts; ++i) {
       if (!is_new(i)) continue;
       float2 x[4];
       values(i, x);
@@ -702,13 +713,13 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
         if (fabsf(x[j].y) < INFINITY) amax = fmaxf(amax, fabsf(x[j].y));
       }
     }
+    amax = shared_max(amax, big_finite);
+    named_bar_sync(1 + (warp >> 1), 64);        // both have read it before the next block's turn
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   const Scale sc = settle<kIsK>(amax, old, kPlain ? 0 : u.s0, err);
   const float2 inv2 = make_float2(sc.inv, sc.inv);
-#pragma unroll(kPlain ? 8 : 1)
-  for (int i = 0; i < kPage / 2; ++i) {
+#pragma unroll(kPlain ? kIts : 1)
+  for (int i = 0; i < kIts; ++i) {
     uint32_t* at0 = reinterpret_cast<uint32_t*>(codes + 2 * i * kHeadDim);
     uint32_t* at1 = at0 + 16;
     if (is_new(i)) {
@@ -735,7 +746,7 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
       *at1 = 0u;
     }
   }
-  if (lane == 0 && (kPlain || u.s0 == 0 || sc.regrow)) *scale_at = sc.now;
+  if (lane == 0 && !(warp & 1) && (kPlain || u.s0 == 0 || sc.regrow)) *scale_at = sc.now;
 }
 
 }  // namespace
@@ -749,7 +760,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
   if (tid == 0) {
     for (int s = 0; s < kStreamStages; ++s) {
       mbar_init(&ctl->full[s], 2);     // the copies' bytes and the table rows
-      mbar_init(&ctl->empty[s], 8);
+      mbar_init(&ctl->empty[s], 16);
     }
     ctl->abort = 0;
     fence_mbar_init();
@@ -762,7 +773,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
   volatile int* abort_flag = &ctl->abort;
   const int H = p.num_kv_heads;
   const int groups = (2 * H + 7) / 8;   // stages of a unit
-  if (warp == 8) {
+  if (warp == 16) {
     uint32_t n = 0;
     bool bad = false;
     for (int i = 0; i < p.units_per_block && !bad; ++i) {
@@ -826,16 +837,17 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
         ctl->abort = 1;
         return;
       }
-      const int r = 8 * y + warp;
-      const uint8_t* rows = smem + s * kStageBytes + warp * (kHeadDim * 2);
+      const int r = 8 * y + (warp >> 1);
+      const uint8_t* rows = smem + s * kStageBytes + (warp >> 1) * (kHeadDim * 2);
       const float4* tab = tabs + s * kStageTab;
+      float* big = ctl->big[n & 1];
       const bool plain = u.s0 == 0 && u.s1 == kPage && (!p.rope || (u.pos >= 0 && u.pos + kPage <= p.n_pos));
       if (r < H) {
-        if (plain) stream_block<true, true>(p, u, rows, tab, r, lane, err);
-        else stream_block<true, false>(p, u, rows, tab, r, lane, err);
+        if (plain) stream_block<true, true>(p, u, rows, tab, r, warp, lane, big, ctl->big_finite, err);
+        else stream_block<true, false>(p, u, rows, tab, r, warp, lane, big, ctl->big_finite, err);
       } else if (r < 2 * H) {
-        if (plain) stream_block<false, true>(p, u, rows, tab, r - H, lane, err);
-        else stream_block<false, false>(p, u, rows, tab, r - H, lane, err);
+        if (plain) stream_block<false, true>(p, u, rows, tab, r - H, warp, lane, big, ctl->big_finite, err);
+        else stream_block<false, false>(p, u, rows, tab, r - H, warp, lane, big, ctl->big_finite, err);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->empty[s]);
@@ -845,10 +857,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
 }
 
 // Queries alone, beside the streamed cache blocks of a call with many tokens.
-__global__ void __launch_bounds__(kAppendThreads) rope_q_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 3) rope_q_kernel(const AppendParams p) {
   __shared__ Tok toks[kMaxTokensPerBlock];
   __shared__ float4 tab[kMaxTokensPerBlock * 32];
-  store_rows<__nv_bfloat16, false>(p, toks, tab, int(blockIdx.x) * p.tokens_per_block, p.tokens_per_block);
+  store_rows<__nv_bfloat16, kHeadDim, false>(p, toks, tab, int(blockIdx.x) * p.tokens_per_block, p.tokens_per_block);
 }
 
 // (cos, sin) of position p and pair i: the angle p * base^(-2 i / d), in fp64,
@@ -866,8 +878,10 @@ __global__ void __launch_bounds__(256) rope_cos_sin_kernel(double base, int half
 // before its own wait, so they release no dependents early and start only once
 // the kernel before them has completed.
 cudaError_t launch_kv_append(const AppendParams& p, int is_f32, int grid, cudaStream_t stream) {
-  return is_f32 ? launch_plain(kv_append_kernel<float>, dim3(grid), dim3(kAppendThreads), 0, stream, p)
-                : launch_plain(kv_append_kernel<__nv_bfloat16>, dim3(grid), dim3(kAppendThreads), 0, stream, p);
+  const auto kernel = !is_f32               ? kv_append_kernel<__nv_bfloat16, 128>
+                      : p.head_dim == 128 ? kv_append_kernel<float, 128>
+                                          : kv_append_kernel<float, 64>;
+  return launch_plain(kernel, dim3(grid), dim3(kAppendThreads), 0, stream, p);
 }
 cudaError_t launch_kv8_append(const AppendParams& p, int grid, cudaStream_t stream) {
   return launch_plain(kv8_append_kernel, dim3(grid), dim3(kAppendThreads), 0, stream, p);

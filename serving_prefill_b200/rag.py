@@ -160,6 +160,7 @@ class KVPool:
         assert self.k.dtype == dtype and self.v.dtype == v_dtype
         self.c = RagKVPool(self.k.data_ptr(), self.v.data_ptr(), num_layers, num_pages, num_kv_heads, PAGE_SIZE,
                            head_dim, RAG_BF16 if dtype == torch.bfloat16 else RAG_F32)
+        self.ref, self.heads, self.dim, self.dev = ctypes.byref(self.c), num_kv_heads, head_dim, self.k.get_device()
 
     @property
     def num_kv_heads(self):
@@ -184,6 +185,7 @@ class KV8Pool:
             assert tuple(t.shape) == sh and t.dtype == d and t.is_contiguous() and t.device == self.k.device
         self.c = RagKV8Pool(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
                             num_layers, num_pages, num_kv_heads, PAGE_SIZE, head_dim)
+        self.ref, self.heads, self.dim, self.dev = ctypes.byref(self.c), num_kv_heads, head_dim, self.k.get_device()
 
     @property
     def num_kv_heads(self):
@@ -209,6 +211,7 @@ class Batch:
                           max(qs, default=0), max(docs, default=0), max(pages, default=0),
                           *[t.data_ptr() for t in self.dev])
         self.doc_lens, self.q_lens = docs, qs
+        self.ref = ctypes.byref(self.c)
 
     @property
     def num_requests(self):
@@ -247,10 +250,9 @@ class Append:
             raise ValueError("tok_off and page_off have one entry more than start, pos0 as many")
         self.dev = [dev(x) for x in (tok_off, start, page_off, page_ids)] + [None if pos0 is None else dev(pos0)]
         self.c = RagAppend(n, total_new, n_pages, *[None if t is None else t.data_ptr() for t in self.dev])
-
-    @property
-    def total_new(self):
-        return self.c.total_new
+        self.ref, self.total_new, self.dev_index = ctypes.byref(self.c), total_new, self.dev[0].get_device()
+        if any(t is not None and t.get_device() != self.dev_index for t in self.dev):
+            raise ValueError("the arrays of an Append are on one device")
 
 
 # --------------------------------------------------------------------------- entry points
@@ -358,47 +360,63 @@ def rag_kv_decode(pool: KVPool, layer: int, chunk_tok_off: torch.Tensor, chunk_p
                                _ptr(device_err), _stream(stream)), "rag_kv_decode")
 
 
-def _need(ok: bool, status: int, where: str):
-    if not ok:
-        raise RagError(status, where)
-
-
-def _on(t: torch.Tensor, stream):
-    """The stream to launch on: the one given, or the current one of the tensor's
-    device. The library launches on the current device, so it has to be that one."""
-    if t.device.index != torch.cuda.current_device():
-        raise RagError(1, f"the tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
-    return _stream(stream)
+def _on(dev: int, stream) -> int:
+    """The stream to launch on (its handle): the one given, or the current one of
+    device `dev`, where the tensors are. The library launches on the current
+    device, so it has to be that one."""
+    if dev != torch._C._cuda_getDevice():
+        raise RagError(1, f"the tensors are on device {dev}, the current one is {torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def rag_rope_cos_sin(base: float, head_dim: int, n_pos: int, device="cuda", stream=None) -> torch.Tensor:
     """Table of rotations [n_pos][head_dim / 2][2] = (cos, sin) of p * base^(-2j/head_dim)."""
     table = torch.empty(max(n_pos, 1), max(head_dim, 2) // 2, 2, device=device)
-    _check(lib().rag_rope_cos_sin(base, head_dim, n_pos, _ptr(table), _on(table, stream)), "rag_rope_cos_sin")
+    _check(lib().rag_rope_cos_sin(base, head_dim, n_pos, _ptr(table), _on(table.get_device(), stream)),
+           "rag_rope_cos_sin")
     return table[:n_pos]
 
 
+def _row_stride(t, rows, heads, dim, dtype, dev, where) -> int:
+    """Elements between the token rows of t [>= rows][heads][dim], each row dense."""
+    n, h, d = t.shape if t.dim() == 3 else (-1, 0, 0)
+    s0, s1, s2 = t.stride() if n >= 0 else (0, 0, 0)
+    if n < rows or h != heads or d != dim:
+        raise RagError(2, where)
+    if t.dtype != dtype or t.get_device() != dev or s2 != 1 or (s1 != d and h != 1):
+        raise RagError(1, where)
+    return s0 if n > 1 else max(s0, h * d)
+
+
 def _append(fn, where, pool, dtype, layer, seqs, k, v, rope, q, q_out, device_err, stream):
-    rows, dim, dev = seqs.c.total_new, pool.c.head_dim, pool.k.device
-
-    def strided(t, heads):
-        _need(t.dim() == 3 and t.shape[0] >= rows and t.shape[2] == dim and (heads is None or t.shape[1] == heads), 2, where)
-        _need(t.dtype == dtype and t.device == dev and t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == dim), 1, where)
-        return max(t.stride(0), t.shape[1] * dim) if t.shape[0] <= 1 else t.stride(0)
-
-    ks, vs = strided(k, pool.c.num_kv_heads), strided(v, pool.c.num_kv_heads)
-    _need((q is None) == (q_out is None), 1, where)
-    qs = hq = 0
+    rows, heads, dim, dev = seqs.total_new, pool.heads, pool.dim, pool.dev
+    ks = _row_stride(k, rows, heads, dim, dtype, dev, where)
+    vs = _row_stride(v, rows, heads, dim, dtype, dev, where)
+    qs = hq = n_pos = 0
+    qp = op = rp = None
     if q is not None:
-        qs, hq = strided(q, None), q.shape[1]
-        _need(q_out.shape == q.shape and q_out.dtype == dtype and q_out.is_contiguous() and q_out.device == dev, 2, where)
-    n_pos = 0
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _row_stride(q, rows, hq, dim, dtype, dev, where)
+        if q_out is None or q_out.dtype != dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
+            raise RagError(1, where)
+        if q_out.shape != q.shape:
+            raise RagError(2, where)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise RagError(1, where)
     if rope is not None:
         n_pos = rope.shape[0]
-        _need(tuple(rope.shape[1:]) == (dim // 2, 2) and rope.dtype == torch.float32 and rope.is_contiguous()
-              and rope.device == dev, 2, where)
-    _check(fn(ctypes.byref(pool.c), layer, ctypes.byref(seqs.c), _ptr(k), ks, _ptr(v), vs, _ptr(rope), n_pos, _ptr(q),
-              qs, hq, _ptr(q_out), _ptr(device_err), _on(k, stream)), where)
+        if rope.shape != (n_pos, dim // 2, 2):
+            raise RagError(2, where)
+        if rope.dtype != torch.float32 or not rope.is_contiguous() or rope.get_device() != dev:
+            raise RagError(1, where)
+        rp = rope.data_ptr()
+    if seqs.dev_index != dev:
+        raise RagError(1, where)
+    status = fn(pool.ref, layer, seqs.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, n_pos, qp, qs, hq, op,
+                None if device_err is None else device_err.data_ptr(), _on(dev, stream))
+    if status != 0:
+        raise RagError(status, where)
 
 
 def rag_kv_append(pool: KVPool, layer: int, seqs: Append, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor = None,
@@ -423,15 +441,27 @@ def rag_kv8_attn(pool: KV8Pool, layer: int, batch: Batch, q: torch.Tensor, o: to
     """Attention of the query tokens q [total_q][num_q_heads][128] (bf16) over their
     requests' pages of an 8-bit pool, into o; causal: query token j of n_q sees
     the first N - n_q + j + 1 of the request's N cached tokens."""
-    where, dev = "rag_kv8_attn", pool.k.device
-    _need(q.dim() == 3 and q.shape[0] >= batch.c.total_q and q.shape[2] == 128 and o.shape == q.shape, 2, where)
-    for t, dt in ((q, torch.bfloat16), (o, torch.bfloat16), (row_lse, torch.float32)):
-        _need(t is None or (t.dtype == dt and t.is_contiguous() and t.device == dev), 1, where)
-    _need(row_lse is None or tuple(row_lse.shape) == tuple(q.shape[:2]), 2, where)
-    _need(workspace.device == dev and workspace.is_contiguous(), 7, where)
-    _check(lib().rag_kv8_attn(ctypes.byref(pool.c), layer, ctypes.byref(batch.c), _ptr(q), q.shape[1], sm_scale,
-                              1 if causal else 0, _ptr(o), _ptr(row_lse), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _on(q, stream)), where)
+    where, dev, hq = "rag_kv8_attn", pool.dev, 0
+    if q.dim() == 3:
+        n, hq, d = q.shape
+    if hq == 0 or d != 128 or n < batch.c.total_q or o.shape != q.shape:
+        raise RagError(2, where)
+    if (q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16 or not q.is_contiguous() or not o.is_contiguous()
+            or q.get_device() != dev or o.get_device() != dev or batch.dev[0].get_device() != dev):
+        raise RagError(1, where)
+    lp = None
+    if row_lse is not None:
+        if row_lse.shape != (n, hq):
+            raise RagError(2, where)
+        if row_lse.dtype != torch.float32 or not row_lse.is_contiguous() or row_lse.get_device() != dev:
+            raise RagError(1, where)
+        lp = row_lse.data_ptr()
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise RagError(7, where)
+    status = lib().rag_kv8_attn(pool.ref, layer, batch.ref, q.data_ptr(), hq, sm_scale, 1 if causal else 0,
+                                o.data_ptr(), lp, workspace.data_ptr(), workspace.nbytes, _on(dev, stream))
+    if status != 0:
+        raise RagError(status, where)
 
 
 def rag_recompute_plan_size(batch: Batch, k_cap: int) -> int:
