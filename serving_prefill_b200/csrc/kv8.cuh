@@ -106,13 +106,24 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, ui
 constexpr int kTile8 = kBN * kHeadDim;       // a K or V tile of codes: 128 rows of 128 B
 constexpr int kPageBytes8 = kPage * kHeadDim;
 
+// What the combine has to merge behind CTA c's first piece (attention kernel ->
+// combine): the unit's rows and the CTAs that hold its pieces.
+struct Kv8Cut {
+  int32_t n_tok;        // query tokens of the unit, 0: nothing begins or goes on here
+  int32_t tok0;         // first of them (row of o)
+  int32_t head0;        // first query head
+  int32_t c0, c1;       // pieces: slot 2 c0 + 1, then slots 2 (c0 + 1) .. 2 c1
+  int32_t pad[3];
+};
+
 struct Kv8Params {
   BatchDev batch;
   int32_t num_pages, num_kv_heads, num_q_heads, group, layer;
-  int32_t tiles_per_split;
   int32_t toks_per_block;          // query tokens of a work unit
-  int32_t item_rows;               // partial rows an item owns
-  int32_t direct;                  // 1: a unit is one item, which writes the output rows itself
+  int32_t item_rows;               // rows of a partial slot
+  int32_t decode;                  // the kernel for at most 16 rows
+  int32_t split_tiles;             // key tiles of a piece, 0: equal stretches
+  int32_t grid;                    // CTAs of the attention kernel
   int32_t causal;
   float scale_log2;
   const float* k_scale;
@@ -122,96 +133,230 @@ struct Kv8Params {
   float* qscale;                   // [total_q][H_q]
   __nv_bfloat16* o;
   float* row_lse;
-  float* part;
-  int32_t* item_prefix;
+  float* part;                     // 2 partial slots per CTA; null: no unit is cut
+  Kv8Cut* cuts;                    // [grid]
   int32_t* err;
-  int64_t max_items;
 };
 
-// Units of a request: blocks of query tokens and splits of the key tiles.
-// Every key comes from the pool, so the tiles are the request's pages alone; a
-// request without pages still has one (empty) item, which writes its zeros.
-__device__ __forceinline__ FwdShape kv8_shape(const Kv8Params& p, const ReqInfo& r) {
-  FwdShape s;
-  if (r.n_q <= 0 || !req_ok(p.batch, r)) { s.n_rt = 0; s.n_split = 0; return s; }
-  s.n_rt = ceil_div(r.n_q, p.toks_per_block);
-  s.n_split = max(1, ceil_div(doc_tiles(r), p.tiles_per_split));
-  return s;
-}
-
-// Key tiles that hold the request's positions 0 .. last_pos.
-__device__ __forceinline__ int tiles_upto(const BatchDev& B, const ReqInfo& r, int last_pos) {
-  const int all = doc_tiles(r);
-  if (last_pos >= r.n_doc - 1) return all;
-  if (last_pos < 0) return 0;
-  int lo = r.c0, hi = r.c1 - 1;   // last chunk that starts at or before last_pos
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(B.chunk_doc_off + mid) - r.doc0 <= last_pos) lo = mid; else hi = mid - 1;
-  }
-  const int page = __ldg(B.chunk_page_off + lo) - r.p0 + (last_pos - (__ldg(B.chunk_doc_off + lo) - r.doc0)) / kPage;
-  return page < 0 ? all : min(all, page / kPagesPerTile + 1);
-}
+// Work decomposition. A unit is (request, KV head, block of query tokens); its
+// key tiles are the request's pages in groups of 8. All units lie on one line,
+// request by request, and each CTA takes a stretch of it. Two measures of the
+// line:
+//   stretches  a unit weighs the time of its tiles and every CTA takes an equal
+//              weight, whatever the requests' lengths: it holds any number of
+//              whole units, whose output rows the CTA writes itself, and at
+//              most two cut ones, whose partial rows go to the CTA's two slots
+//              (dealing out equal splits of every unit left the busiest SM with
+//              1.65 times the average work on 16 ragged requests)
+//   pieces     a unit weighs its pieces of split_tiles tiles at most, and a CTA
+//              takes one (any number when no unit is cut): with few units no
+//              CTA pays for the start and end of two. If the pieces turn out to
+//              be more than the CTAs, stretches are used after all.
+// One warp of a CTA walks the stretch and hands the items to the others
+// through a ring in shared memory.
+constexpr int kCost2 = 5, kCost1 = 3;      // weight of a key tile with two Q tiles and with one
+constexpr int kMinWork = 2 * kCost2;       // least stretch of a CTA: two tiles
+constexpr int kMinWorkDecode = 2;
+constexpr int kReqCache = 16;              // requests whose geometry stays in shared memory
+constexpr int kItemSlots = 4;
 
 struct Kv8Item {
-  int b, g, rb, split;
-  int t_begin, t_end;
-  ReqInfo req;
+  int32_t n;            // key tiles, 0: no more items
+  int32_t t_begin;
+  int32_t g, rb;
+  int32_t slot;         // partial slot, -1: the unit is whole
+  int32_t q0, n_q, n_doc;
 };
 
-__device__ __forceinline__ Kv8Item kv8_item(const Kv8Params& p, const int32_t* prefix, int w) {
-  int lo = 0, hi = p.batch.num_requests - 1;
-  while (lo < hi) {  // last b with prefix[b] <= w
-    const int mid = (lo + hi + 1) >> 1;
-    if (prefix[mid] <= w) lo = mid; else hi = mid - 1;
-  }
-  Kv8Item it;
-  it.b = lo;
-  it.req = load_req(p.batch, lo);
-  const FwdShape sh = kv8_shape(p, it.req);
-  int local = w - prefix[lo];
-  it.rb = local % sh.n_rt;
-  local /= sh.n_rt;
-  it.split = local % sh.n_split;
-  it.g = local / sh.n_split;
-  int n_tiles = doc_tiles(it.req);
-  if (p.causal && it.rb < sh.n_rt - 1)
-    n_tiles = tiles_upto(p.batch, it.req, it.req.n_doc - it.req.n_q + (it.rb + 1) * p.toks_per_block - 1);
-  it.t_begin = min(it.split * p.tiles_per_split, n_tiles);
-  it.t_end = min(it.t_begin + p.tiles_per_split, n_tiles);
-  return it;
+struct Kv8Ring {
+  uint64_t full[kItemSlots], empty[kItemSlots];
+  Kv8Item item[kItemSlots];
+  int32_t total, ctas, pieces;   // the line: weight, CTAs that share it, 1: measured in pieces
+  ReqInfo req[kReqCache];
+};
+
+__device__ __forceinline__ int kv8_blocks(const Kv8Params& p, const ReqInfo& r) {
+  return r.n_q <= 0 || !req_ok(p.batch, r) ? 0 : ceil_div(r.n_q, p.toks_per_block);
+}
+// Key tiles of block rb, at least one (a request without pages writes its zeros
+// from a fully masked tile). Causal: the pages behind the block's last visible
+// key are left out; a page holds at most 16 of the tokens that lie behind it,
+// so floor(tokens / 16) whole pages do.
+__device__ __forceinline__ int kv8_tiles(const Kv8Params& p, const ReqInfo& r, int rb) {
+  int pages = r.n_pages;
+  if (p.causal) pages -= min(max(r.n_q - (rb + 1) * p.toks_per_block, 0), r.n_doc) / kPage;
+  return max(1, ceil_div(pages, kPagesPerTile));
+}
+__device__ __forceinline__ int kv8_cost(const Kv8Params& p, const ReqInfo& r, int rb) {
+  if (p.decode) return 1;
+  return r.n_q - rb * p.toks_per_block > p.toks_per_block / kQTiles ? kCost2 : kCost1;
+}
+__device__ __forceinline__ int kv8_weight(const Kv8Params& p, const ReqInfo& r, int rb, bool pieces) {
+  const int n = kv8_tiles(p, r, rb);
+  return pieces ? ceil_div(n, p.split_tiles) : n * kv8_cost(p, r, rb);
+}
+// Weight of one KV head of a request.
+__device__ __forceinline__ int kv8_head_work(const Kv8Params& p, const ReqInfo& r, bool pieces) {
+  const int n = kv8_blocks(p, r);
+  int w = 0;
+  for (int rb = 0; rb < n; ++rb) w += kv8_weight(p, r, rb, pieces);
+  return w;
+}
+__device__ __forceinline__ ReqInfo kv8_req(const Kv8Params& p, const Kv8Ring* ring, int b) {
+  return b < kReqCache ? ring->req[b] : load_req(p.batch, b);
 }
 
-// Items of every request as an exclusive prefix in shared memory (one warp).
-// Returns the total, 0 (reported) when it exceeds what the workspace holds.
-__device__ __forceinline__ int kv8_prefix(const Kv8Params& p, int32_t* prefix, int lane) {
+// The line of the batch (one warp): each request's weight as an exclusive
+// prefix, the total, the CTAs that share it.
+__device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv8Ring* ring, int lane) {
   const int B = p.batch.num_requests;
-  int carry = 0;
-  for (int base = 0; base < B; base += 32) {
-    const int b = base + lane;
-    int cnt = 0;
-    if (b < B) {
-      const ReqInfo r = load_req(p.batch, b);
-      if (!req_ok(p.batch, r) && blockIdx.x == 0) atomicOr(p.err, kDevErrGeometry);
-      const FwdShape sh = kv8_shape(p, r);
-      cnt = p.num_kv_heads * sh.n_split * sh.n_rt;
+  const bool one_piece_each = p.part != nullptr;   // cut units: one piece a CTA
+  bool pieces = p.split_tiles > 0;
+  for (int base = 0; base < min(B, kReqCache); base += 32)
+    if (base + lane < min(B, kReqCache)) ring->req[base + lane] = load_req(p.batch, base + lane);
+  __syncwarp();
+  int64_t carry = 0;   // 31 bits for every batch that agrees with its host totals
+  for (int round = 0; round < 2; ++round) {
+    carry = 0;
+    for (int base = 0; base < B; base += 32) {
+      const int b = base + lane;
+      int64_t cnt = 0;
+      if (b < B) {
+        const ReqInfo r = kv8_req(p, ring, b);
+        if (!req_ok(p.batch, r) && blockIdx.x == 0) atomicOr(p.err, kDevErrGeometry);
+        cnt = int64_t(p.num_kv_heads) * kv8_head_work(p, r, pieces);
+      }
+      int64_t incl = cnt;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (b < B) prefix[b] = int(carry + incl - cnt);
+      carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    int incl = cnt;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (b < B) prefix[b] = carry + incl - cnt;
-    carry += __shfl_sync(0xffffffffu, incl, 31);
+    if (!(pieces && one_piece_each && carry > p.grid)) break;
+    pieces = false;
   }
   __syncwarp();
-  if (carry > p.max_items) {
-    if (blockIdx.x == 0 && lane == 0) atomicOr(p.err, kDevErrGeometry);
-    carry = 0;
+  if (carry > INT32_MAX) {
+    if (lane == 0 && blockIdx.x == 0) atomicOr(p.err, kDevErrGeometry);
     for (int b = lane; b < B; b += 32) prefix[b] = 0;
+    carry = 0;
   }
-  if (lane == 0) prefix[B] = carry;
-  return carry;
+  if (lane == 0) {
+    const int W = int(carry);
+    const int most = pieces ? W : W / (p.decode ? kMinWorkDecode : kMinWork);
+    prefix[B] = W;
+    ring->total = W;
+    ring->ctas = max(1, min(most, p.grid));
+    ring->pieces = pieces ? 1 : 0;
+  }
+  __syncwarp();
+}
+
+// The items of one CTA in order (warp-uniform).
+struct Kv8Walk {
+  int pos, end, b, per_head;
+  ReqInfo req;
+  Kv8Cut cut;
+
+  __device__ __forceinline__ void start(const Kv8Ring* ring) {
+    const int W = ring->total, C = ring->ctas, c = int(blockIdx.x);
+    pos = end = 0;
+    b = -1;
+    per_head = 1;
+    cut = {};
+    if (W == 0 || c >= C) return;
+    pos = int(int64_t(c) * W / C);
+    end = int(int64_t(c + 1) * W / C);
+  }
+  __device__ __forceinline__ bool next(const Kv8Params& p, const int32_t* prefix, const Kv8Ring* ring, Kv8Item& it) {
+    const bool pieces = ring->pieces != 0;
+    while (pos < end) {
+      if (b < 0 || prefix[b + 1] <= pos) {
+        int lo = b < 0 ? 0 : b + 1, hi = p.batch.num_requests - 1;
+        while (lo < hi) {  // last request with prefix <= pos
+          const int mid = (lo + hi + 1) >> 1;
+          if (prefix[mid] <= pos) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        req = kv8_req(p, ring, b);
+        per_head = kv8_head_work(p, req, pieces);
+      }
+      int rem = pos - prefix[b];
+      it.g = rem / per_head;
+      rem -= it.g * per_head;
+      it.rb = 0;
+      int w = kv8_weight(p, req, 0, pieces);
+      while (rem >= w) {
+        rem -= w;
+        w = kv8_weight(p, req, ++it.rb, pieces);
+      }
+      const int s = pos - rem, n = kv8_tiles(p, req, it.rb), cost = kv8_cost(p, req, it.rb);
+      int t_begin, t_end;
+      if (pieces) {
+        t_begin = int(int64_t(rem) * n / w);
+        t_end = int(int64_t(rem + 1) * n / w);
+        pos += 1;
+      } else {
+        t_begin = ceil_div(rem, cost);
+        t_end = min(n, ceil_div(end - s, cost));
+        pos = s + w;
+      }
+      if (t_begin >= t_end) continue;   // the stretch ends or begins inside the last tile
+      const int cta = int(blockIdx.x);
+      it.slot = t_begin > 0 ? 2 * cta : t_end < n ? 2 * cta + 1 : -1;
+      it.t_begin = t_begin;
+      it.n = t_end - t_begin;
+      it.q0 = req.q0;
+      it.n_q = req.n_q;
+      it.n_doc = req.n_doc;
+      if (t_begin > 0) {
+        // a piece that goes on from another CTA's: the second of its unit reports the cut
+        const int64_t W = ring->total, C = ring->ctas;
+        const int c0 = int((int64_t(s + 1) * C - 1) / W);
+        const int last = pieces ? s + w - 1 : s + (n - 1) * cost;   // the last piece, or tile, begins here
+        if (cta == c0 + 1) {
+          cut.n_tok = min(p.toks_per_block, req.n_q - it.rb * p.toks_per_block);
+          cut.tok0 = req.q0 + it.rb * p.toks_per_block;
+          cut.head0 = it.g * p.group;
+          cut.c0 = c0;
+          cut.c1 = int((int64_t(last + 1) * C - 1) / W);
+        }
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ void kv8_ring_init(Kv8Ring* ring, int readers) {
+  for (int s = 0; s < kItemSlots; ++s) {
+    mbar_init(&ring->full[s], 1);
+    mbar_init(&ring->empty[s], readers);
+  }
+}
+// The walking warp hands out its j-th item (n = 0: the end). False: a wait gave up.
+__device__ __forceinline__ bool kv8_put(Kv8Ring* ring, uint32_t j, const Kv8Item& it, int lane, volatile int* abort) {
+  const int s = j % kItemSlots;
+  if (j >= kItemSlots && !mbar_wait(&ring->empty[s], (j / kItemSlots - 1) & 1, abort)) return false;
+  if (lane == 0) {
+    ring->item[s] = it;
+    mbar_arrive(&ring->full[s]);
+  }
+  __syncwarp();
+  return true;
+}
+// A reading warp (kWarp), or a reading thread, takes the j-th item. False: the
+// end, or a wait gave up (bad = 1).
+template <bool kWarp>
+__device__ __forceinline__ bool kv8_take(Kv8Ring* ring, uint32_t j, Kv8Item& it, volatile int* abort, int& bad) {
+  const int s = j % kItemSlots;
+  if (!mbar_wait(&ring->full[s], (j / kItemSlots) & 1, abort)) { bad = 1; return false; }
+  it = ring->item[s];
+  if (kWarp) __syncwarp();   // every lane has the item before the slot is given back
+  if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ring->empty[s]);
+  return it.n > 0;
 }
 
 // The page that lane `lane & 7` of a producer warp loads for a tile, and its
@@ -238,6 +383,6 @@ cudaError_t launch_kv8_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const C
 // query blocks of at most 16 rows
 cudaError_t launch_kv8_decode(const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p, int grid,
                               cudaStream_t stream);
-cudaError_t launch_kv8_combine(const Kv8Params& p, int max_q, cudaStream_t stream);
+cudaError_t launch_kv8_combine(const Kv8Params& p, cudaStream_t stream);
 
 }  // namespace rag

@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 
 #include "rag_prefill.h"
 #include "host.cuh"
@@ -79,81 +78,61 @@ static rag_status check_append(AppendParams& p, int elem, int num_layers, int la
 // ------------------------------------------------------------ attention
 
 struct Kv8Plan {
-  int decode;   // query blocks of at most 16 rows: the transposed kernel
-  int tiles_per_split, direct, grid, toks_per_block, item_rows;
-  int64_t max_items;
+  int decode;        // query blocks of at most 16 rows: the transposed kernel
+  int split_tiles;   // key tiles of a piece, 0: equal stretches
+  int cut;           // units may be cut: partial rows and a combine
+  int grid, toks_per_block, item_rows;
 };
 
-// Split the key tiles of every unit (request, KV head, block of query tokens)
-// so that the work fills the SMs. Every split length is tried; the cost of one
-// is, for one request (alike items), ceil(items / SMs) of them after one
-// another, for several the list-scheduling bound (average load per SM plus one
-// longest item), an item's start and end counted as two tiles.
-static Kv8Plan plan_kv8_uncached(const rag_batch& b, int num_kv_heads, int group, int sms) {
+// Units of at most this many key tiles are not cut: one CTA walks them in less
+// time than the combine's launch and its reads of partial rows take.
+constexpr int kWholeTiles = 2, kWholeTilesDecode = 2;
+// A piece's start and end (first loads, last products, its rows), in tiles.
+constexpr double kPieceTiles = 4.0;
+
+static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
   Kv8Plan pl;
   pl.decode = int64_t(b.max_q) * group <= 16 ? 1 : 0;
   pl.toks_per_block = pl.decode ? 16 / group : kQTiles * (kBM / group);
   pl.item_rows = pl.decode ? 16 : kFwdRows;
-  if (pl.decode) sms *= 2;   // two CTAs share an SM
-  const double overhead = pl.decode ? 4.0 : 2.0;
-  const int B = std::max(1, b.num_requests);
+  // two CTAs of the decode kernel share an SM; no more CTAs than the batch's
+  // capacities can give work to
   const int tiles_max = std::max(1, cdiv(b.max_pages, kPagesPerTile));
-  const int rt_avg = std::max(1, cdiv(cdiv(b.total_q, B), pl.toks_per_block));
-  const int tiles_avg = std::max(1, cdiv(cdiv(b.num_page_refs, B), kPagesPerTile));
-  const double units = double(num_kv_heads) * B * rt_avg;
-  double best = 1e300;
-  int best_ts = tiles_max;
-  for (int ts = std::min(2, tiles_max); ts <= tiles_max; ++ts) {
-    const double items = units * cdiv(tiles_avg, ts);
-    const double cost = B == 1 ? std::ceil(items / sms) * (std::min(ts, tiles_avg) + overhead)
-                               : (units * tiles_avg + items * overhead) / sms + std::min(ts, tiles_avg) + overhead;
-    if (cost < best + 1e-9) {   // ties go to the longer split (fewer partial rows)
-      best = cost;
-      best_ts = ts;
-    }
+  pl.cut = tiles_max > (pl.decode ? kWholeTilesDecode : kWholeTiles) ? 1 : 0;
+  const double rt = cdiv(b.max_q, pl.toks_per_block);
+  const double most = !pl.cut ? double(num_kv_heads) * (cdiv(b.total_q, pl.toks_per_block) + b.num_requests)
+                              : num_kv_heads * rt * (double(b.num_page_refs) / kPagesPerTile + 2.0 * b.num_requests) *
+                                    (pl.decode ? 1 : kCost2) / (pl.decode ? kMinWorkDecode : kMinWork);
+  pl.grid = int(std::max(1.0, std::min(double(pl.decode ? 2 * sms : sms), most)));
+  pl.split_tiles = tiles_max;
+  if (pl.cut) {
+    // One piece a CTA, or equal stretches with up to two pieces' starts and
+    // ends in a CTA. Requests of unlike lengths round up to half a piece a
+    // unit more; if that is not enough on the device, it uses stretches.
+    const double B = std::max(1, b.num_requests);
+    const double units = num_kv_heads * B * std::max(1, cdiv(cdiv(b.total_q, int(B)), pl.toks_per_block));
+    const double tiles = B == 1 ? tiles_max : double(b.num_page_refs) / kPagesPerTile / B + 0.5;
+    const double room = B == 1 ? std::floor(pl.grid / units) : pl.grid / units - 0.5;
+    const double ts = room >= 1.0 ? std::ceil(tiles / room) : 0.0;
+    pl.split_tiles = ts > 0.0 && ts + kPieceTiles <= units * tiles / pl.grid + 2 * kPieceTiles ? std::max(2, int(ts)) : 0;
   }
-  pl.tiles_per_split = best_ts;
-  pl.direct = best_ts >= tiles_max ? 1 : 0;
-  const int64_t rt_bound = cdiv(b.total_q, pl.toks_per_block) + int64_t(b.num_requests);
-  pl.max_items = int64_t(num_kv_heads) * rt_bound * cdiv(tiles_max, best_ts);
-  pl.grid = int(std::max<int64_t>(1, std::min<int64_t>(sms, pl.max_items)));
   return pl;
 }
 
-// The plan reads only these totals and the shape, so the last few are kept per
-// host thread (every layer of a step, every step of a batch has the same).
-static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
-  struct Key {
-    int32_t v[8];
-  };
-  constexpr int kKept = 8;
-  thread_local Key keys[kKept];
-  thread_local Kv8Plan plans[kKept];
-  thread_local int n = 0, next = 0;
-  const Key k = {{b.num_requests, b.max_pages, b.max_q, b.total_q, b.num_page_refs, num_kv_heads, group, sms}};
-  for (int i = 0; i < n; ++i)
-    if (std::memcmp(&keys[i], &k, sizeof(Key)) == 0) return plans[i];
-  const Kv8Plan pl = plan_kv8_uncached(b, num_kv_heads, group, sms);
-  const int slot = n < kKept ? n++ : (next++ % kKept);
-  keys[slot] = k;
-  plans[slot] = pl;
-  return pl;
-}
-
-// Workspace (bytes, each region 256-aligned): error word, item prefix, split
-// queries, their row scales, partial rows (none when a unit is one item).
+// Workspace (bytes, each region 256-aligned): error word, split queries, their
+// row scales, the cuts, two partial slots per CTA (when units are cut).
 struct Kv8Ws {
-  size_t off_prefix, off_qs, off_qscale, off_part, total;
+  size_t off_qs, off_qscale, off_cuts, off_part, total;
 };
 static Kv8Ws ws_kv8(const rag_batch& b, int num_q_heads, const Kv8Plan& pl) {
   Kv8Ws w;
   const size_t rows = pl.decode ? 0 : size_t(b.total_q) * num_q_heads;   // the decode kernel splits its own queries
   size_t at = 256;
-  w.off_prefix = at; at = align256(at + sizeof(int32_t) * (size_t(b.num_requests) + 1));
   w.off_qs = at; at = align256(at + rows * 2 * kHeadDim);
   w.off_qscale = at; at = align256(at + rows * sizeof(float));
+  w.off_cuts = at; at = align256(at + (pl.cut ? size_t(pl.grid) * sizeof(Kv8Cut) : 0));
   w.off_part = at;
-  if (!pl.direct) at = align256(at + size_t(pl.max_items) * pl.item_rows * kPartStride * sizeof(float));
+  if (pl.cut) at = align256(at + size_t(2) * pl.grid * pl.item_rows * kPartStride * sizeof(float));
   w.total = at;
   return w;
 }
@@ -164,7 +143,13 @@ static rag_status check_kv8_attn(const rag_kv8_pool* pool, const rag_batch* batc
   st = check_batch(batch);
   if (st != RAG_OK) return st;
   if (num_q_heads <= 0 || num_q_heads % pool->num_kv_heads != 0) return RAG_ERR_SHAPE;
-  if (num_q_heads / pool->num_kv_heads > kBM) return RAG_ERR_UNSUPPORTED;
+  const int G = num_q_heads / pool->num_kv_heads;
+  if (G > kBM) return RAG_ERR_UNSUPPORTED;
+  // the units' weights are counted in 31 bits
+  const rag_batch& b = *batch;
+  const int toks = plan_kv8(b, pool->num_kv_heads, G, 1).toks_per_block;
+  const double tiles = double(b.num_page_refs) / kPagesPerTile + 2.0 * b.num_requests;
+  if (tiles * pool->num_kv_heads * (double(cdiv(b.max_q, toks)) + 1) * kCost2 >= 2147483648.0) return RAG_ERR_UNSUPPORTED;
   return RAG_OK;
 }
 
@@ -297,10 +282,11 @@ rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch
   p.num_q_heads = num_q_heads;
   p.group = G;
   p.layer = layer;
-  p.tiles_per_split = pl.tiles_per_split;
   p.toks_per_block = pl.toks_per_block;
   p.item_rows = pl.item_rows;
-  p.direct = pl.direct;
+  p.decode = pl.decode;
+  p.split_tiles = pl.split_tiles;
+  p.grid = pl.grid;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(float(kHeadDim))) * 1.4426950408889634f;
   p.k_scale = pool->k_scale;
@@ -310,10 +296,9 @@ rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch
   p.qscale = reinterpret_cast<float*>(base + ws.off_qscale);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.row_lse = row_lse;
-  p.part = reinterpret_cast<float*>(base + ws.off_part);
-  p.item_prefix = reinterpret_cast<int32_t*>(base + ws.off_prefix);
+  p.part = pl.cut ? reinterpret_cast<float*>(base + ws.off_part) : nullptr;
+  p.cuts = reinterpret_cast<Kv8Cut*>(base + ws.off_cuts);
   p.err = reinterpret_cast<int32_t*>(base);
-  p.max_items = pl.max_items;
 
   CUtensorMap tm_q, tm_k, tm_v;
   {
@@ -344,9 +329,9 @@ rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch
     ls.done(e);
     if (e != cudaSuccess) return RAG_ERR_CUDA;
   }
-  if (!pl.direct) {
+  if (pl.cut) {
     LaunchScope ls(kKindKv8Combine, s);
-    cudaError_t e = launch_kv8_combine(p, b.max_q, s);
+    cudaError_t e = launch_kv8_combine(p, s);
     ls.done(e);
     if (e != cudaSuccess) return RAG_ERR_CUDA;
   }

@@ -63,13 +63,13 @@ struct Ctrl {
   uint64_t desc_full[kDescSlots], desc_empty[kDescSlots];
   TileDesc desc[kDescSlots];
   ChunkCache chunks;
+  Kv8Ring ring;
   alignas(8) uint8_t vnv[kVSt][kPagesPerTile];   // valid slots of a V stage's pages
   float sq[2][kRows];                 // row scale of Q times the softmax scale (log2)
   alignas(16) float red[2][kRows][4]; // per-tile row maxima of the four key warps, by tile parity
   alignas(16) float lsum[kRows][4];   // per-item row sums of the four key warps
   uint32_t tmem_base;
   int32_t abort;
-  int32_t total_items;
 };
 
 static_assert(offsetof(Ctrl, vnv) % 8 == 0 && offsetof(Ctrl, red) % 16 == 0 && offsetof(Ctrl, lsum) % 16 == 0,
@@ -153,7 +153,6 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int B = p.batch.num_requests;
   const int G = p.group;
 
   pdl_launch_dependents();
@@ -179,6 +178,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       mbar_init(&ctl->desc_full[s], 1);
       mbar_init(&ctl->desc_empty[s], 4);   // one arrival per key warp
     }
+    kv8_ring_init(&ctl->ring, 7);   // 4 key warps, MMA, V and Q warps
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -187,21 +187,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     tmem_relinquish();
   }
   if (warp == 4 && lane == 0) { tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
-  if (warp == 0) {
-    const int total = kv8_prefix(p, prefix, lane);
-    if (lane == 0) ctl->total_items = total;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (blockIdx.x == 0) {
-    pdl_wait();   // the previous call's combine may still read the offsets
-    for (int b = tid; b <= B; b += blockDim.x) p.item_prefix[b] = prefix[b];
-  }
-
-  const int total_items = ctl->total_items;
   const uint32_t tmem = ctl->tmem_base;
   volatile int* abort_flag = &ctl->abort;
+  Kv8Item it = {};
+  uint32_t n_it = 0;   // items taken
 
   if (warp < 4) {
     // ------------------------------------------------------------ key warps: thread = key of the tile
@@ -209,20 +201,20 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const uint32_t lane_off = uint32_t(warp * 32) << 16;
     uint32_t t_glob = 0, n_items = 0;
     // One item with its rows padded to R; returns false when a wait gave up.
-    auto run_item = [&](auto Rc, const Kv8Item& it, int w, int n) -> bool {
+    auto run_item = [&](auto Rc, int n) -> bool {
       constexpr int R = decltype(Rc)::value;
       constexpr int NO = (3 * R + 7) / 8 * 8;   // O^T columns in use, to the next 8
-      const int rows = it.req.n_q * G;
+      const int rows = it.n_q * G;
       float mm[R], ls[R];                       // reference max less kTop; row sum
 #pragma unroll
       for (int r = 0; r < R; ++r) { mm[r] = -INFINITY; ls[r] = 0.f; }
       uint32_t ov[NO];
 #pragma unroll
       for (int j = 0; j < NO; ++j) ov[j] = 0u;
-      if (n > 0) {
+      {
         if (!mbar_wait(&ctl->q_full[n_items & 1], (n_items >> 1) & 1, abort_flag)) return false;
         const float* sq = ctl->sq[n_items & 1];
-        const int first = p.causal ? it.req.n_doc - it.req.n_q : it.req.n_doc;   // row r sees positions <= first + r / G
+        const int first = p.causal ? it.n_doc - it.n_q : it.n_doc;   // row r sees positions <= first + r / G
         for (int i = 0; i < n; ++i) {
           const uint32_t t = t_glob + i;
           const uint32_t slot = t % kDescSlots;
@@ -338,13 +330,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const float sum = fmaf(__uint_as_float(ov[2 * R + r]), 0.00390625f,
                                fmaf(__uint_as_float(ov[R + r]), 0.0625f, __uint_as_float(ov[r])));
-        if (p.direct) {
-          const int64_t row = int64_t(it.req.q0 + r / G) * p.num_q_heads + it.g * G + r % G;
+        if (it.slot < 0) {
+          const int64_t row = int64_t(it.q0 + r / G) * p.num_q_heads + it.g * G + r % G;
           p.o[row * kHeadDim + d] = __float2bfloat16_rn(sum * inv);
           if (d == r && p.row_lse)
             p.row_lse[row] = ((mm[r] == -INFINITY ? 0.f : mm[r]) + __log2f(l)) * 0.69314718055994531f;
         } else {
-          float* dst = p.part + (size_t(w) * p.item_rows + r) * kPartStride;
+          float* dst = p.part + (size_t(it.slot) * p.item_rows + r) * kPartStride;
           reinterpret_cast<__half*>(dst)[d] = __float2half_rn(sum * inv);
           if (d == r) reinterpret_cast<float4*>(dst + kHeadDim / 2)[0] = make_float4(mm[r], l, 0.f, 0.f);
         }
@@ -352,13 +344,12 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       return true;
     };
     int bad = 0;
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-      const Kv8Item it = kv8_item(p, prefix, w);
-      const int n = it.t_end - it.t_begin;
-      const int R = pad_rows(it.req.n_q * G);   // at most 16 rows on this path
-      const bool ok = R == 4   ? run_item(std::integral_constant<int, 4>{}, it, w, n)
-                      : R == 8 ? run_item(std::integral_constant<int, 8>{}, it, w, n)
-                               : run_item(std::integral_constant<int, 16>{}, it, w, n);
+    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      const int n = it.n;
+      const int R = pad_rows(it.n_q * G);   // at most 16 rows on this path
+      const bool ok = R == 4   ? run_item(std::integral_constant<int, 4>{}, n)
+                      : R == 8 ? run_item(std::integral_constant<int, 8>{}, n)
+                               : run_item(std::integral_constant<int, 16>{}, n);
       if (!ok) bad = 1;
     }
     if (bad) raise_abort(ctl, p.err);
@@ -366,28 +357,35 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // ------------------------------------------------------------ producer
     uint32_t t_glob = 0, n_k = 0, n_v = 0;   // n_k, n_v: K and V tiles issued
     int bad = 0;
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-      const Kv8Item it = kv8_item(p, prefix, w);
-      const int n = it.t_end - it.t_begin;
-      if (n == 0) continue;
-      __syncwarp();
-      load_chunk_cache(&ctl->chunks, p.batch, it.req, lane);
+    Kv8Walk walk;
+    int cached_b = -1;
+    kv8_line(p, prefix, &ctl->ring, lane);
+    walk.start(&ctl->ring);
+    while (!bad && walk.next(p, prefix, &ctl->ring, it)) {
+      if (!kv8_put(&ctl->ring, n_it++, it, lane, abort_flag)) { bad = 1; break; }
+      const int n = it.n;
       const int sub = lane & 7;
       auto page_id = [&](int tile) {
-        return lane < 16 ? load_page_id(p.batch, it.req, tile * kPagesPerTile + sub) : -1;
+        return lane < 16 ? load_page_id(p.batch, walk.req, tile * kPagesPerTile + sub) : -1;
       };
       auto resolve = [&](int tile, int32_t id) {
         PageRef pg;
         pg.page = -1; pg.nvalid = 0; pg.lstart = 0; pg.chunk = -1;
         if (lane < 16)
-          pg = page_ref_cached(&ctl->chunks, p.batch, it.req, tile * kPagesPerTile + sub, id, p.num_pages,
+          pg = page_ref_cached(&ctl->chunks, p.batch, walk.req, tile * kPagesPerTile + sub, id, p.num_pages,
                                lane < 8 ? p.err : nullptr);
         return pg;
       };
       // page ids run two tiles ahead, scales one
-      PageRef pg = resolve(it.t_begin, page_id(it.t_begin));
-      float sc = page_scale_load(p, pg, it.g, lane);
+      const int32_t first_id = page_id(it.t_begin);
       int32_t next_id = n > 1 ? page_id(it.t_begin + 1) : -1;
+      if (walk.b != cached_b) {
+        __syncwarp();
+        load_chunk_cache(&ctl->chunks, p.batch, walk.req, lane);
+        cached_b = walk.b;
+      }
+      PageRef pg = resolve(it.t_begin, first_id);
+      float sc = page_scale_load(p, pg, it.g, lane);
       for (int i = 0; i < n; ++i) {
         const uint32_t t = t_glob + i;
         const int tile = it.t_begin + i;
@@ -436,6 +434,12 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       }
       t_glob += n;
     }
+    it.n = 0;
+    if (!bad && !kv8_put(&ctl->ring, n_it, it, lane, abort_flag)) bad = 1;
+    if (p.part) {
+      pdl_wait();   // the previous call's combine may still read the cuts
+      if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
+    }
     if (bad) raise_abort(ctl, p.err);
     // let every copy this warp issued land before the CTA exits
     if (lane == 0 && ctl->abort) {
@@ -447,9 +451,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // ------------------------------------------------------------ V slots without a token -> 0
     uint32_t t_glob = 0;
     int bad = 0;
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-      const Kv8Item it = kv8_item(p, prefix, w);
-      const int n = it.t_end - it.t_begin;
+    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      const int n = it.n;
       for (int i = 0; i < n; ++i) {
         const uint32_t t = t_glob + i;
         const int sv = t % kVSt;
@@ -476,10 +479,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     uint32_t q_iter = 0;
     int bad = 0;
     pdl_wait();               // q may be the previous kernel's output
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-      const Kv8Item it = kv8_item(p, prefix, w);
-      if (it.t_end == it.t_begin) continue;
-      const int rows = it.req.n_q * G, R = pad_rows(rows);
+    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      const int rows = it.n_q * G, R = pad_rows(rows);
       const int buf = int(q_iter & 1u);
       if (q_iter >= 2 && !mbar_wait(&ctl->q_empty[buf], ((q_iter >> 1) - 1) & 1, abort_flag)) { bad = 1; break; }
       uint8_t* dst = sQ + buf * kQBytes;
@@ -492,7 +493,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         for (int j = 0; j < 16; ++j) x[j] = 0.f;
         if (r < rows) {
           const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + ((int64_t(it.req.q0) + r / G) * p.num_q_heads + it.g * G + r % G) * kHeadDim + 16 * c);
+              p.q + ((int64_t(it.q0) + r / G) * p.num_q_heads + it.g * G + r % G) * kHeadDim + 16 * c);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint4 v = src[h];
@@ -544,11 +545,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     if (lane == 0) {
       uint32_t t_glob = 0, n_items = 0;
       int bad = 0;
-      for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-        const Kv8Item it = kv8_item(p, prefix, w);
-        const int n = it.t_end - it.t_begin;
-        if (n == 0) continue;
-        const int R = pad_rows(it.req.n_q * G);
+      while (!bad && kv8_take<false>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+        const int n = it.n;
+        const int R = pad_rows(it.n_q * G);
         const uint32_t idesc_qk = idesc_e4m3_f32(kBN, uint32_t(n_qk(R)), 0, 0);
         const uint32_t idesc_pv = idesc_e4m3_f32(kHeadDim, uint32_t(n_pv(R)), 1, 0);
         const int qb = int(n_items & 1u);

@@ -4,8 +4,8 @@
 // scale of the page and KV head, and the query tokens' own keys were appended
 // to it).
 //
-// One persistent CTA per SM walks work items (request, KV head, two 128-row Q
-// tiles, split of the key tiles); a row is (query token, head in the group),
+// One persistent CTA per SM walks its stretch of the work units (request, KV head,
+// two 128-row Q tiles; their key tiles); a row is (query token, head in the group),
 // 128 / G tokens to a tile. The scores come from the codes themselves:
 //   q = s_q (hi + lo), hi and lo e4m3, s_q a power of two per row, split once
 //       by kv8_split_q_kernel: a bf16 value's 8 significant bits are two e4m3
@@ -75,12 +75,16 @@ struct Ctrl {
   TileDesc desc[kDescSlots];
   VInfo vinfo[kRSt];
   ChunkCache chunks;
+  Kv8Ring ring;
   uint32_t tmem_base;
   int32_t abort;
-  int32_t total_items;
 };
 
 constexpr size_t kSmemData = size_t(kQTiles) * kQTileBytes + size_t(kKSt + kRSt) * kTile8 + size_t(kVSt) * kVTile;
+constexpr size_t smem_bytes(int num_requests) {
+  return 1024 + kSmemData + sizeof(Ctrl) + sizeof(int32_t) * (size_t(num_requests) + 1);
+}
+static_assert(smem_bytes(kMaxRequests) <= 227 * 1024, "shared memory of a CTA");
 
 __device__ __forceinline__ void raise_abort(Ctrl* c, int32_t* err) {
   if (!c->abort) {
@@ -122,7 +126,6 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  const int B = p.batch.num_requests;
   const int G = p.group;
   const int TT = p.toks_per_block / kQTiles;   // query tokens of a Q tile
 
@@ -147,6 +150,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       mbar_init(&ctl->desc_full[s], 1);
       mbar_init(&ctl->desc_empty[s], 8);   // one arrival per softmax warp
     }
+    kv8_ring_init(&ctl->ring, 11);   // 8 softmax warps, MMA, 2 convert warps
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -155,21 +159,13 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tmem_relinquish();
   }
   if (warp == 8 && lane == 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
-  if (warp == 0) {
-    const int total = kv8_prefix(p, prefix, lane);
-    if (lane == 0) ctl->total_items = total;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (blockIdx.x == 0) {
-    pdl_wait();   // the previous call's combine may still read the offsets
-    for (int b = tid; b <= B; b += blockDim.x) p.item_prefix[b] = prefix[b];
-  }
-
-  const int total_items = ctl->total_items;
   const uint32_t tmem = ctl->tmem_base;
   volatile int* abort_flag = &ctl->abort;
+  Kv8Item it = {};
+  uint32_t n_it = 0;   // items taken
 
   // The pool and the batch are read at once; the split queries, which the
   // kernel before this one writes, and every output only after pdl_wait.
@@ -187,20 +183,19 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint32_t n_of = 0;              // items whose O_qt has been read
     int bad = 0;
     pdl_wait();                     // the row scales come from the kernel before this one
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-      const Kv8Item it = kv8_item(p, prefix, w);
-      const int n = it.t_end - it.t_begin;
+    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      const int n = it.n;
       // One Q tile: warpgroup 0 alone, alternating between the two S buffers
       // so that S of the next tile is computed during this tile's softmax.
       const int tok0 = it.rb * p.toks_per_block;
-      const int n_qt = it.req.n_q - tok0 > TT ? 2 : 1;
+      const int n_qt = it.n_q - tok0 > TT ? 2 : 1;
       const bool single = n_qt == 1;
       const bool active = qt < n_qt;
       const int tok = tok0 + qt * TT + r / G;
       const int head = it.g * G + r % G;
-      const bool row_valid = active && r < TT * G && tok < it.req.n_q;
-      const int64_t row = int64_t(it.req.q0 + tok) * p.num_q_heads + head;
-      const int lim = p.causal ? it.req.n_doc - it.req.n_q + tok : it.req.n_doc - 1;   // last visible position
+      const bool row_valid = active && r < TT * G && tok < it.n_q;
+      const int64_t row = int64_t(it.q0 + tok) * p.num_q_heads + head;
+      const int lim = p.causal ? it.n_doc - it.n_q + tok : it.n_doc - 1;   // last visible position
       const float c_row = row_valid ? p.scale_log2 * __ldcg(p.qscale + row) : 0.f;
       const bool warp_live = __any_sync(0xffffffffu, row_valid);
       float m_ref = -INFINITY, l_sum = 0.f;
@@ -349,39 +344,30 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       if (!active) continue;
 
       // ---- epilogue: O of this Q tile
-      if (n > 0) {
-        // the MMA warp commits o_full once per item after the item's last PV
-        if (!mbar_wait(&ctl->o_full[qt], n_of & 1, abort_flag)) { bad = 1; break; }
-        ++n_of;
-        tc_fence_after();
-      }
+      // the MMA warp commits o_full once per item after the item's last PV
+      if (!mbar_wait(&ctl->o_full[qt], n_of & 1, abort_flag)) { bad = 1; break; }
+      ++n_of;
+      tc_fence_after();
       if (!warp_live) {   // no row of this warp is read or written
-        if (n > 0) {
-          tc_fence_before();
-          mbar_arrive(&ctl->o_free[qt]);
-        }
+        tc_fence_before();
+        mbar_arrive(&ctl->o_free[qt]);
         continue;
       }
       float o[kHeadDim];
-      if (n > 0) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t u[32];
-          tmem_ld32(o_addr + 32 * c, u);
-          tmem_wait_ld();
+      for (int c = 0; c < 4; ++c) {
+        uint32_t u[32];
+        tmem_ld32(o_addr + 32 * c, u);
+        tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[32 * c + j] = __uint_as_float(u[j]);
-        }
-        tc_fence_before();
-        mbar_arrive(&ctl->o_free[qt]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kHeadDim; ++j) o[j] = 0.f;
+        for (int j = 0; j < 32; ++j) o[32 * c + j] = __uint_as_float(u[j]);
       }
+      tc_fence_before();
+      mbar_arrive(&ctl->o_free[qt]);
       // l = 0: the row saw no key of this item; a row of nan (a nan query) keeps it
       const float inv = l_sum == 0.f ? 0.f : 1.f / l_sum;
       if (!row_valid) continue;
-      if (p.direct) {
+      if (it.slot < 0) {
         uint4* dst = reinterpret_cast<uint4*>(p.o + row * kHeadDim);
 #pragma unroll
         for (int c = 0; c < kHeadDim / 8; ++c) {
@@ -395,9 +381,9 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
         if (p.row_lse) p.row_lse[row] = (m_use + __log2f(l_sum)) * 0.69314718055994531f;
       } else {
-        // partial row: this split's own softmax average O/l in fp16 (|O/l| is
+        // partial row: this piece's own softmax average O/l in fp16 (|O/l| is
         // bounded by max |V|), then its reference max m and sum l in fp32
-        uint4* dst = reinterpret_cast<uint4*>(p.part + (size_t(w) * p.item_rows + qt * kBM + r) * kPartStride);
+        uint4* dst = reinterpret_cast<uint4*>(p.part + (size_t(it.slot) * p.item_rows + qt * kBM + r) * kPartStride);
 #pragma unroll
         for (int c = 0; c < kHeadDim / 8; ++c) {
           uint4 v;
@@ -417,29 +403,35 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       // ------------------------------------------------------------ producer
       uint32_t t_glob = 0, n_k = 0, n_v = 0;   // n_k, n_v: K and V tiles issued
       int bad = 0;
-      for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-        const Kv8Item it = kv8_item(p, prefix, w);
-        const int n = it.t_end - it.t_begin;
-        if (n == 0) continue;
-        load_chunk_cache(&ctl->chunks, p.batch, it.req, lane);
+      Kv8Walk walk;
+      int cached_b = -1;
+      kv8_line(p, prefix, &ctl->ring, lane);
+      walk.start(&ctl->ring);
+      while (!bad && walk.next(p, prefix, &ctl->ring, it)) {
+        if (!kv8_put(&ctl->ring, n_it++, it, lane, abort_flag)) { bad = 1; break; }
+        const int n = it.n;
         const int sub = lane & 7;
-        const int n_ref = doc_tiles(it.req) * kPagesPerTile;   // page references past the request's pages load nothing
         auto page_id = [&](int tile) {
-          const int ref = tile * kPagesPerTile + sub;
-          return lane < 16 && ref < n_ref ? load_page_id(p.batch, it.req, ref) : -1;
+          return lane < 16 ? load_page_id(p.batch, walk.req, tile * kPagesPerTile + sub) : -1;
         };
         auto resolve = [&](int tile, int32_t id) {
           PageRef pg;
           pg.page = -1; pg.nvalid = 0; pg.lstart = 0; pg.chunk = -1;
           if (lane < 16)
-            pg = page_ref_cached(&ctl->chunks, p.batch, it.req, tile * kPagesPerTile + sub, id, p.num_pages,
+            pg = page_ref_cached(&ctl->chunks, p.batch, walk.req, tile * kPagesPerTile + sub, id, p.num_pages,
                                  lane < 8 ? p.err : nullptr);
           return pg;
         };
         // page ids run two tiles ahead, scales one
-        PageRef pg = resolve(it.t_begin, page_id(it.t_begin));
-        float sc = page_scale_load(p, pg, it.g, lane);
+        const int32_t first_id = page_id(it.t_begin);
         int32_t next_id = n > 1 ? page_id(it.t_begin + 1) : -1;
+        if (walk.b != cached_b) {
+          __syncwarp();
+          load_chunk_cache(&ctl->chunks, p.batch, walk.req, lane);
+          cached_b = walk.b;
+        }
+        PageRef pg = resolve(it.t_begin, first_id);
+        float sc = page_scale_load(p, pg, it.g, lane);
         for (int i = 0; i < n; ++i) {
           const uint32_t t = t_glob + i;
           const int tile = it.t_begin + i;
@@ -490,6 +482,12 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         t_glob += n;
       }
+      it.n = 0;
+      if (!bad && !kv8_put(&ctl->ring, n_it, it, lane, abort_flag)) bad = 1;
+      if (p.part) {
+        pdl_wait();   // the previous call's combine may still read the cuts
+        if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
+      }
       if (bad) raise_abort(ctl, p.err);
       // let every copy this warp issued land before the CTA exits
       if (lane == 0 && ctl->abort) {
@@ -509,21 +507,19 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const int c = lane & 7;                         // 16 codes: columns 16c .. 16c + 15
       uint32_t t_glob = 0, q_iter = 0;
       int bad = 0;
-      for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-        const Kv8Item it = kv8_item(p, prefix, w);
-        const int n = it.t_end - it.t_begin;
-        if (n == 0) continue;
+      while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+        const int n = it.n;
         if (warp == 10) {
           if (q_iter > 0 && !mbar_wait(&ctl->q_empty, (q_iter - 1) & 1, abort_flag)) { bad = 1; break; }
           if (lane == 0) {
             pdl_wait();
             const int tok0 = it.rb * p.toks_per_block;
-            const int n_qt = it.req.n_q - tok0 > TT ? 2 : 1;
+            const int n_qt = it.n_q - tok0 > TT ? 2 : 1;
             mbar_arrive_expect_tx(&ctl->q_full, n_qt * 2 * TT * G * kHeadDim);
             for (int q = 0; q < n_qt; ++q) {
-              tma_load_3d(sQ + q * kQTileBytes, &tm_q, &ctl->q_full, 0, it.g * G, it.req.q0 + tok0 + q * TT);
+              tma_load_3d(sQ + q * kQTileBytes, &tm_q, &ctl->q_full, 0, it.g * G, it.q0 + tok0 + q * TT);
               tma_load_3d(sQ + q * kQTileBytes + kTile8, &tm_q, &ctl->q_full, kHeadDim, it.g * G,
-                          it.req.q0 + tok0 + q * TT);
+                          it.q0 + tok0 + q * TT);
             }
           }
           ++q_iter;
@@ -592,11 +588,9 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           for (int kk = 0; kk < 4; ++kk)
             mma_ss_f8(tmem + d, code_desc(qb + kTile8, kk), code_desc(kb, kk), idesc_qk, 1);
         };
-        for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
-          const Kv8Item it = kv8_item(p, prefix, w);
-          const int n = it.t_end - it.t_begin;
-          if (n == 0) continue;
-          const int n_qt = it.req.n_q - it.rb * p.toks_per_block > TT ? 2 : 1;
+        while (!bad && kv8_take<false>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+          const int n = it.n;
+          const int n_qt = it.n_q - it.rb * p.toks_per_block > TT ? 2 : 1;
           if (!mbar_wait(&ctl->q_full, q_iter & 1, abort_flag)) { bad = 1; break; }
           tc_fence_after();
           if (n_qt == 1) {
@@ -780,70 +774,72 @@ __global__ void __launch_bounds__(256) kv8_split_q_kernel(const Kv8Params p, int
   if (c == 0) p.qscale[row] = odd ? __int_as_float(0x7fffffff) : pow2f(e);
 }
 
-// Merge the split partials (O, m, l) of every row:
+// Merge the partial rows (O, m, l) of every cut unit:
 //   m = max_s m_s, l = sum_s l_s 2^(m_s - m), O = sum_s O_s l_s 2^(m_s - m) / l.
-// One warp per output row (query token, head), each lane 4 of the 128 columns;
-// lane j holds the statistics of split s0 + j, the O slices of up to 16 splits
-// are requested before any is used. grid: x = groups of 8 rows, y = request.
-constexpr int kCombineBatch = 16;
+// Block (c, y) merges rows 32 y .. 32 y + 31 of the unit whose second piece CTA
+// c left (nothing for other CTAs); a warp takes a row at a time, each lane 4 of
+// the 128 columns; lane j holds the statistics of piece s0 + j, and the O
+// slices of kCombineBatch pieces are requested before any is used. (A warp per
+// output row of the batch, each finding its own pieces, took 45 us on 16
+// requests of 32-128 tokens.)
+constexpr int kCombineBatch = 8;
+constexpr int kCombineRows = 32;
 
 __global__ void __launch_bounds__(256, 4) kv8_combine_kernel(const Kv8Params p) {
   pdl_launch_dependents();
-  const int b = blockIdx.y;
+  pdl_wait();   // partials and cuts come from the attention kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const ReqInfo req = load_req(p.batch, b);
-  const FwdShape sh = kv8_shape(p, req);
-  const int idx = blockIdx.x * 8 + warp;
-  const int tok = idx / p.num_q_heads, head = idx % p.num_q_heads;
-  pdl_wait();   // partials and item offsets come from the attention kernel
-  if (sh.n_rt == 0 || tok >= req.n_q) return;   // uniform over the warp
-  const int G = p.group, g = head / G;
-  const int rb = tok / p.toks_per_block, in = tok % p.toks_per_block;
-  const int TT = p.item_rows > kBM ? p.toks_per_block / kQTiles : p.toks_per_block;   // tokens of a Q tile
-  const int rr = (in / TT) * kBM + (in % TT) * G + head % G;
-  const int base = b == 0 ? 0 : __ldcg(p.item_prefix + b);
-  const size_t first = size_t(base) + size_t(g) * sh.n_split * sh.n_rt + rb;
-  if (first + size_t(sh.n_split - 1) * sh.n_rt >= size_t(p.max_items)) return;
-  const float* row0 = p.part + (first * p.item_rows + rr) * kPartStride;
-  const size_t split_stride = size_t(sh.n_rt) * p.item_rows * kPartStride;
-  constexpr int kStatOff = kHeadDim / 2;   // 32-bit word of m (then l) in a row
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < sh.n_split; s0 += kCombineBatch) {
-    const float2 ml = (lane < kCombineBatch && s0 + lane < sh.n_split)
-                          ? __ldcg(reinterpret_cast<const float2*>(row0 + (s0 + lane) * split_stride + kStatOff))
-                          : make_float2(-INFINITY, 0.f);
-    uint2 v[kCombineBatch];
+  const int4 c4 = __ldcg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x));
+  const int c1 = __ldcg(&p.cuts[blockIdx.x].c1);
+  const int n_tok = c4.x, tok0 = c4.y, head0 = c4.z, c0 = c4.w;
+  if (n_tok == 0) return;
+  const int G = p.group;
+  const int TT = p.decode ? p.toks_per_block : p.toks_per_block / kQTiles;   // tokens of a Q tile
+  const int n_piece = c1 - c0 + 1;
+  const size_t slot = size_t(p.item_rows) * kPartStride;
+  for (int rr = blockIdx.y * kCombineRows + warp; rr < min(p.item_rows, int(blockIdx.y + 1) * kCombineRows); rr += 8) {
+    const int r = rr % kBM, tok = rr / kBM * TT + r / G;
+    if (r >= TT * G || tok >= n_tok) continue;   // uniform over the warp
+    const float* row0 = p.part + size_t(2 * c0) * slot + size_t(rr) * kPartStride;
+    auto piece = [&](int i) { return row0 + (i == 0 ? slot : size_t(2 * i) * slot); };
+    constexpr int kStatOff = kHeadDim / 2;   // 32-bit word of m (then l) in a row
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < n_piece; s0 += kCombineBatch) {
+      const float2 ml = (lane < kCombineBatch && s0 + lane < n_piece)
+                            ? __ldcg(reinterpret_cast<const float2*>(piece(s0 + lane) + kStatOff))
+                            : make_float2(-INFINITY, 0.f);
+      uint2 v[kCombineBatch];
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j)
-      v[j] = s0 + j < sh.n_split ? __ldcg(reinterpret_cast<const uint2*>(row0 + (s0 + j) * split_stride) + lane)
-                                 : make_uint2(0u, 0u);
-    float mb = fmaxf(m, ml.x);
-    for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-    const float mu = (mb == -INFINITY) ? 0.f : mb;
-    if (s0 > 0) {
-      const float sc = (m == -INFINITY) ? 0.f : ex2(m - mu);
-      l *= sc;
-      acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
-    }
-    m = mb;
-    const float wl = (ml.x == -INFINITY) ? ml.y : ml.y * ex2(ml.x - mu);   // l = 0 there, or nan
+      for (int j = 0; j < kCombineBatch; ++j)
+        v[j] = s0 + j < n_piece ? __ldcg(reinterpret_cast<const uint2*>(piece(s0 + j)) + lane) : make_uint2(0u, 0u);
+      float mb = fmaxf(m, ml.x);
+      for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+      const float mu = (mb == -INFINITY) ? 0.f : mb;
+      if (s0 > 0) {
+        const float sc = (m == -INFINITY) ? 0.f : ex2(m - mu);
+        l *= sc;
+        acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
+      }
+      m = mb;
+      const float wl = (ml.x == -INFINITY) ? ml.y : ml.y * ex2(ml.x - mu);   // l = 0 there, or nan
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j) {
-      const float wgt = __shfl_sync(0xffffffffu, wl, j);
-      const float2 lo = f16x2_to_f32x2(v[j].x), hi = f16x2_to_f32x2(v[j].y);
-      l += wgt;
-      acc.x += lo.x * wgt; acc.y += lo.y * wgt; acc.z += hi.x * wgt; acc.w += hi.y * wgt;
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const float wgt = __shfl_sync(0xffffffffu, wl, j);
+        const float2 lo = f16x2_to_f32x2(v[j].x), hi = f16x2_to_f32x2(v[j].y);
+        l += wgt;
+        acc.x += lo.x * wgt; acc.y += lo.y * wgt; acc.z += hi.x * wgt; acc.w += hi.y * wgt;
+      }
     }
+    const float m_use = (m == -INFINITY) ? 0.f : m;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t orow = int64_t(tok0 + tok) * p.num_q_heads + head0 + r % G;
+    uint2 out;
+    out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+    reinterpret_cast<uint2*>(p.o + orow * kHeadDim)[lane] = out;
+    if (lane == 0 && p.row_lse) p.row_lse[orow] = (m_use + __log2f(l)) * 0.69314718055994531f;
   }
-  const float m_use = (m == -INFINITY) ? 0.f : m;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t orow = int64_t(req.q0 + tok) * p.num_q_heads + head;
-  uint2 out;
-  out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-  out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(p.o + orow * kHeadDim)[lane] = out;
-  if (lane == 0 && p.row_lse) p.row_lse[orow] = (m_use + __log2f(l)) * 0.69314718055994531f;
 }
 
 // ---------------------------------------------------------------- launchers
@@ -855,17 +851,16 @@ cudaError_t launch_kv8_split_q(const Kv8Params& p, cudaStream_t stream) {
 
 cudaError_t launch_kv8_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p,
                            int grid, cudaStream_t stream) {
-  const size_t smem = 1024 + f8::kSmemData + sizeof(f8::Ctrl) + sizeof(int32_t) * (p.batch.num_requests + 1) + 64;
+  const size_t smem = f8::smem_bytes(p.batch.num_requests);
   static SmemAttr attr;
   cudaError_t e = ensure_smem_attr(kv8_fwd_kernel, attr, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv8_fwd_kernel, dim3(grid), dim3(f8::kThreads), smem, stream, 1, tq, tk, tv, p);
 }
 
-cudaError_t launch_kv8_combine(const Kv8Params& p, int max_q, cudaStream_t stream) {
-  const int64_t rows = int64_t(max_q) * p.num_q_heads;
-  return launch_pdl(kv8_combine_kernel, dim3(unsigned((rows + 7) / 8), p.batch.num_requests), dim3(256), 0, stream, 1,
-                    p);
+cudaError_t launch_kv8_combine(const Kv8Params& p, cudaStream_t stream) {
+  return launch_pdl(kv8_combine_kernel, dim3(p.grid, (p.item_rows + kCombineRows - 1) / kCombineRows), dim3(256), 0,
+                    stream, 1, p);
 }
 
 }  // namespace rag
