@@ -87,14 +87,59 @@ cudaError_t launch_rope_cos_sin(double base, int head_dim, int n_pos, float2* ta
 
 // ------------------------------------------------------------ attention
 
-// D(tmem) (+)= A(smem desc) * B(smem desc), 8-bit operands, 32 values of k a step.
-__device__ __forceinline__ void mma_ss_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+// The issuing warp runs its loops whole, with one lane elected for the products
+// themselves: in a branch of one lane every operand would be moved to the
+// uniform registers that tcgen05.mma reads, for each of a tile's products anew.
+// For the same reason descriptors are built as a low word (address, leading
+// offset), stepped by an addition, and a constant high word (stride, version,
+// 128-byte swizzle). (One lane and whole descriptors: the issuing thread alone
+// took 2,900 of a tile's 3,400 cycles, of which the products need 1,450.)
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);
+}
+constexpr uint32_t kSdescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row atoms 1 KB apart, 128B swizzle
+
+// D(tmem) (+)= A(smem) * B(smem), 8-bit operands, 32 values of k a step; by the
+// elected lane.
+__device__ __forceinline__ void mma_ss_f8(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 a, {%2, %6};\n\t"
+      "mov.b64 b, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%1], a, b, %4, p;\n\t}\n" ::"r"(leader),
+      "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kSdescHi)
+      : "memory");
+}
+// D(tmem) (+)= A(tmem, fp16) * B(smem, fp16), 16 values of k a step.
+__device__ __forceinline__ void mma_ts_f16(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%3, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, p;\n\t}\n" ::"r"(leader),
+      "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kSdescHi)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_by(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(leader),
+      "r"(smem_u32(bar))
       : "memory");
 }
 // Instruction descriptor for kind::f8f6f4 with e4m3 A and B, fp32 accumulator.
@@ -103,7 +148,8 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, ui
   return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-constexpr int kTile8 = kBN * kHeadDim;       // a K or V tile of codes: 128 rows of 128 B
+constexpr int kTile8 = kBN * kHeadDim;       // a K or V tile of codes of the decode kernel: 128 rows of 128 B
+constexpr int kFwdPages = 5;                 // pages of a key tile of the prompt kernel
 constexpr int kPageBytes8 = kPage * kHeadDim;
 
 // What the combine has to merge behind CTA c's first piece (attention kernel ->
@@ -139,7 +185,7 @@ struct Kv8Params {
 };
 
 // Work decomposition. A unit is (request, KV head, block of query tokens); its
-// key tiles are the request's pages in groups of 8. All units lie on one line,
+// key tiles are the request's pages in groups of 8 (decode) or 5. All units lie on one line,
 // request by request, and each CTA takes a stretch of it. Two measures of the
 // line:
 //   stretches  a unit weighs the time of its tiles and every CTA takes an equal
@@ -182,10 +228,11 @@ __device__ __forceinline__ int kv8_blocks(const Kv8Params& p, const ReqInfo& r) 
 // from a fully masked tile). Causal: the pages behind the block's last visible
 // key are left out; a page holds at most 16 of the tokens that lie behind it,
 // so floor(tokens / 16) whole pages do.
+__host__ __device__ constexpr int kv8_tile_pages(int decode) { return decode ? kPagesPerTile : kFwdPages; }
 __device__ __forceinline__ int kv8_tiles(const Kv8Params& p, const ReqInfo& r, int rb) {
   int pages = r.n_pages;
   if (p.causal) pages -= min(max(r.n_q - (rb + 1) * p.toks_per_block, 0), r.n_doc) / kPage;
-  return max(1, ceil_div(pages, kPagesPerTile));
+  return max(1, ceil_div(pages, kv8_tile_pages(p.decode)));
 }
 __device__ __forceinline__ int kv8_cost(const Kv8Params& p, const ReqInfo& r, int rb) {
   if (p.decode) return 1;
@@ -359,23 +406,69 @@ __device__ __forceinline__ bool kv8_take(Kv8Ring* ring, uint32_t j, Kv8Item& it,
   return it.n > 0;
 }
 
-// The page that lane `lane & 7` of a producer warp loads for a tile, and its
-// scale (lanes 0-7: K's, lanes 8-15: V's). A scale outside (0, inf), or of V
+// The pages of an item, resolved by the producer warp a window of kTiles tiles
+// (up to 32 pages, one a lane) at a time: page ids run two windows ahead and
+// scales one, so that no tile waits for a load. (Resolved tile by tile, with
+// ids two tiles and scales one tile ahead, every tile cost a load's latency:
+// 2 us a tile of 80 or of 128 keys alike.) A scale outside (0, inf), or of V
 // above 128, is reported and taken as 1.
-struct PageScale {
-  PageRef pg;
-  float scale;
+template <int kPagesTile>
+struct Kv8Pages {
+  static constexpr int kTiles = 32 / kPagesTile;
+  int base, next_id;          // first page reference of the item; id of this lane's page two windows on
+  PageRef cur, nxt;
+  float cur_k, cur_v, nxt_k, nxt_v;
+
+  __device__ __forceinline__ int ref(int window, int lane) const {
+    return base + window * (kTiles * kPagesTile) + lane;
+  }
+  __device__ __forceinline__ int id(const Kv8Params& p, const ReqInfo& r, int window, int lane) const {
+    return lane < kTiles * kPagesTile ? load_page_id(p.batch, r, ref(window, lane)) : -1;
+  }
+  __device__ __forceinline__ PageRef resolve(const Kv8Params& p, const ReqInfo& r, const ChunkCache* cc, int window,
+                                             int id, int lane) const {
+    PageRef pg;
+    pg.page = -1; pg.nvalid = 0; pg.lstart = 0; pg.chunk = -1;
+    if (lane < kTiles * kPagesTile) pg = page_ref_cached(cc, p.batch, r, ref(window, lane), id, p.num_pages, p.err);
+    return pg;
+  }
+  __device__ __forceinline__ void scales(const Kv8Params& p, const PageRef& pg, int g, float& k, float& v) const {
+    k = v = 1.f;
+    if (pg.page < 0 || pg.nvalid <= 0) return;
+    const int64_t at = (int64_t(p.layer) * p.num_pages + pg.page) * p.num_kv_heads + g;
+    k = __ldg(p.k_scale + at);
+    v = __ldg(p.v_scale + at);
+  }
+  __device__ __forceinline__ void settle(const Kv8Params& p) {
+    if (!(cur_k > 0.f && cur_k < INFINITY)) { atomicOr(p.err, kDevErrRange); cur_k = 1.f; }
+    if (!(cur_v > 0.f && cur_v <= 128.f)) { atomicOr(p.err, kDevErrRange); cur_v = 1.f; }
+  }
+  __device__ __forceinline__ void start(const Kv8Params& p, const ReqInfo& r, ChunkCache* cc, bool load_chunks,
+                                        int t_begin, int g, int lane) {
+    base = t_begin * kPagesTile;
+    const int id0 = id(p, r, 0, lane), id1 = id(p, r, 1, lane);
+    next_id = id(p, r, 2, lane);
+    if (load_chunks) {
+      __syncwarp();
+      load_chunk_cache(cc, p.batch, r, lane);
+    }
+    cur = resolve(p, r, cc, 0, id0, lane);
+    scales(p, cur, g, cur_k, cur_v);
+    nxt = resolve(p, r, cc, 1, id1, lane);
+    scales(p, nxt, g, nxt_k, nxt_v);
+  }
+  // tile i of the item begins a window (i > 0)
+  __device__ __forceinline__ void advance(const Kv8Params& p, const ReqInfo& r, const ChunkCache* cc, int i, int g,
+                                          int lane) {
+    const int w = i / kTiles;
+    cur = nxt;
+    cur_k = nxt_k;
+    cur_v = nxt_v;
+    nxt = resolve(p, r, cc, w + 1, next_id, lane);
+    scales(p, nxt, g, nxt_k, nxt_v);
+    next_id = id(p, r, w + 2, lane);
+  }
 };
-__device__ __forceinline__ float page_scale_load(const Kv8Params& p, const PageRef& pg, int g, int lane) {
-  if (pg.page < 0 || pg.nvalid <= 0 || lane >= 16) return 1.f;
-  const float* at = (lane < 8 ? p.k_scale : p.v_scale) + (int64_t(p.layer) * p.num_pages + pg.page) * p.num_kv_heads + g;
-  return __ldg(at);
-}
-__device__ __forceinline__ float page_scale_ok(const Kv8Params& p, float s, int lane) {
-  if (s > 0.f && s <= (lane < 8 ? 3.3e38f : 128.f)) return s;
-  atomicOr(p.err, kDevErrRange);
-  return 1.f;
-}
 
 cudaError_t launch_kv8_split_q(const Kv8Params&, cudaStream_t);
 cudaError_t launch_kv8_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Kv8Params& p,

@@ -97,11 +97,12 @@ static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms
   pl.item_rows = pl.decode ? 16 : kFwdRows;
   // two CTAs of the decode kernel share an SM; no more CTAs than the batch's
   // capacities can give work to
-  const int tiles_max = std::max(1, cdiv(b.max_pages, kPagesPerTile));
+  const int pages = kv8_tile_pages(pl.decode);
+  const int tiles_max = std::max(1, cdiv(b.max_pages, pages));
   pl.cut = tiles_max > (pl.decode ? kWholeTilesDecode : kWholeTiles) ? 1 : 0;
   const double rt = cdiv(b.max_q, pl.toks_per_block);
   const double most = !pl.cut ? double(num_kv_heads) * (cdiv(b.total_q, pl.toks_per_block) + b.num_requests)
-                              : num_kv_heads * rt * (double(b.num_page_refs) / kPagesPerTile + 2.0 * b.num_requests) *
+                              : num_kv_heads * rt * (double(b.num_page_refs) / pages + 2.0 * b.num_requests) *
                                     (pl.decode ? 1 : kCost2) / (pl.decode ? kMinWorkDecode : kMinWork);
   pl.grid = int(std::max(1.0, std::min(double(pl.decode ? 2 * sms : sms), most)));
   pl.split_tiles = tiles_max;
@@ -111,7 +112,7 @@ static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms
     // unit more; if that is not enough on the device, it uses stretches.
     const double B = std::max(1, b.num_requests);
     const double units = num_kv_heads * B * std::max(1, cdiv(cdiv(b.total_q, int(B)), pl.toks_per_block));
-    const double tiles = B == 1 ? tiles_max : double(b.num_page_refs) / kPagesPerTile / B + 0.5;
+    const double tiles = B == 1 ? tiles_max : double(b.num_page_refs) / pages / B + 0.5;
     const double room = B == 1 ? std::floor(pl.grid / units) : pl.grid / units - 0.5;
     const double ts = room >= 1.0 ? std::ceil(tiles / room) : 0.0;
     pl.split_tiles = ts > 0.0 && ts + kPieceTiles <= units * tiles / pl.grid + 2 * kPieceTiles ? std::max(2, int(ts)) : 0;
@@ -147,9 +148,9 @@ static rag_status check_kv8_attn(const rag_kv8_pool* pool, const rag_batch* batc
   if (G > kBM) return RAG_ERR_UNSUPPORTED;
   // the units' weights are counted in 31 bits
   const rag_batch& b = *batch;
-  const int toks = plan_kv8(b, pool->num_kv_heads, G, 1).toks_per_block;
-  const double tiles = double(b.num_page_refs) / kPagesPerTile + 2.0 * b.num_requests;
-  if (tiles * pool->num_kv_heads * (double(cdiv(b.max_q, toks)) + 1) * kCost2 >= 2147483648.0) return RAG_ERR_UNSUPPORTED;
+  const Kv8Plan pl = plan_kv8(b, pool->num_kv_heads, G, 1);
+  const double tiles = double(b.num_page_refs) / kv8_tile_pages(pl.decode) + 2.0 * b.num_requests;
+  if (tiles * pool->num_kv_heads * (double(cdiv(b.max_q, pl.toks_per_block)) + 1) * kCost2 >= 2147483648.0) return RAG_ERR_UNSUPPORTED;
   return RAG_OK;
 }
 

@@ -119,11 +119,10 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-// Rows of 128 codes (128 B), 128B-swizzled, K-major: k-step kk covers codes [32 kk, 32 kk + 32).
-__device__ __forceinline__ uint64_t kmajor(uint32_t base, int kk) { return sdesc_sw128(base + kk * 32, 16, 1024); }
-// The V tile [128 keys][128 d] read as the MN-major A operand V^T (M = d: one
-// 128-byte atom): k-step kk covers keys [32 kk, 32 kk + 32), 8-key groups 1 KB apart.
-__device__ __forceinline__ uint64_t vt_desc(uint32_t base, int kk) { return sdesc_sw128(base + kk * 32 * 128, 0, 1024); }
+// Low words of the operands' descriptors: K, Q and P tiles are K-major rows of
+// 128 codes, a k-step of 32 codes is 32 bytes on (2 in units of 16). The V tile
+// [128 keys][128 d] is the MN-major A operand V^T (M = d: one 128-byte atom, no
+// leading offset), a k-step of 32 keys is 4 KB on.
 // Byte of (row n, column k) in a tile of 128-byte rows, 128B-swizzled.
 __device__ __forceinline__ uint32_t swz(int n, int k) {
   return uint32_t((n >> 3) * 1024 + (n & 7) * 128 + (((k >> 4) ^ (n & 7)) << 4) + (k & 15));
@@ -365,39 +364,19 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (!kv8_put(&ctl->ring, n_it++, it, lane, abort_flag)) { bad = 1; break; }
       const int n = it.n;
       const int sub = lane & 7;
-      auto page_id = [&](int tile) {
-        return lane < 16 ? load_page_id(p.batch, walk.req, tile * kPagesPerTile + sub) : -1;
-      };
-      auto resolve = [&](int tile, int32_t id) {
-        PageRef pg;
-        pg.page = -1; pg.nvalid = 0; pg.lstart = 0; pg.chunk = -1;
-        if (lane < 16)
-          pg = page_ref_cached(&ctl->chunks, p.batch, walk.req, tile * kPagesPerTile + sub, id, p.num_pages,
-                               lane < 8 ? p.err : nullptr);
-        return pg;
-      };
-      // page ids run two tiles ahead, scales one
-      const int32_t first_id = page_id(it.t_begin);
-      int32_t next_id = n > 1 ? page_id(it.t_begin + 1) : -1;
-      if (walk.b != cached_b) {
-        __syncwarp();
-        load_chunk_cache(&ctl->chunks, p.batch, walk.req, lane);
-        cached_b = walk.b;
-      }
-      PageRef pg = resolve(it.t_begin, first_id);
-      float sc = page_scale_load(p, pg, it.g, lane);
+      Kv8Pages<kPagesPerTile> pages;
+      pages.start(p, walk.req, &ctl->chunks, walk.b != cached_b, it.t_begin, it.g, lane);
+      cached_b = walk.b;
       for (int i = 0; i < n; ++i) {
         const uint32_t t = t_glob + i;
-        const int tile = it.t_begin + i;
-        const PageRef cur = pg;
-        const float cur_sc = sc;
-        if (i + 1 < n) {
-          pg = resolve(tile + 1, next_id);
-          sc = page_scale_load(p, pg, it.g, lane);
-          next_id = i + 2 < n ? page_id(tile + 2) : -1;
-        }
+        const int wi = i % Kv8Pages<kPagesPerTile>::kTiles;
+        if (wi == 0 && i > 0) pages.advance(p, walk.req, &ctl->chunks, i, it.g, lane);
+        const int from = wi * kPagesPerTile + sub;
+        const int page = __shfl_sync(0xffffffffu, pages.cur.page, from);
+        const int nvalid = __shfl_sync(0xffffffffu, pages.cur.nvalid, from);
+        const int lstart = __shfl_sync(0xffffffffu, pages.cur.lstart, from);
         // the boxes first: they need the page alone, the descriptor its scales
-        const int box = cur.page >= 0 ? ((p.layer * p.num_pages + cur.page) * p.num_kv_heads + it.g) * kPage
+        const int box = page >= 0 ? ((p.layer * p.num_pages + page) * p.num_kv_heads + it.g) * kPage
                                       : -kPage;   // fully out of range: the box is zero-filled
         const int s = t % kKSt;
         if (t >= uint32_t(kKSt) && !mbar_wait(&ctl->kempty[s], ((t / kKSt) - 1) & 1, abort_flag)) { bad = 1; break; }
@@ -412,20 +391,21 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           break;
         }
         TileDesc* d = &ctl->desc[slot];
-        const float scale = page_scale_ok(p, cur_sc, lane);
+        if (wi == 0) pages.settle(p);
+        const float ks = __shfl_sync(0xffffffffu, pages.cur_k, from), vs = __shfl_sync(0xffffffffu, pages.cur_v, from);
         if (lane < 8) {
-          d->ks[sub] = scale;
-          d->lstart[sub] = cur.lstart;
-          d->nvalid[sub] = uint8_t(cur.nvalid);
+          d->ks[sub] = ks;
+          d->lstart[sub] = lstart;
+          d->nvalid[sub] = uint8_t(nvalid);
         } else if (lane < 16) {
-          d->lv[sub] = __log2f(scale);
-          d->iv[sub] = __frcp_rn(scale);
+          d->lv[sub] = __log2f(vs);
+          d->iv[sub] = __frcp_rn(vs);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->desc_full[slot]);
         const int sv = t % kVSt;
         if (t >= uint32_t(kVSt) && !mbar_wait(&ctl->vempty[sv], ((t / kVSt) - 1) & 1, abort_flag)) { bad = 1; break; }
-        if (lane >= 8 && lane < 16) ctl->vnv[sv][sub] = uint8_t(cur.nvalid);
+        if (lane >= 8 && lane < 16) ctl->vnv[sv][sub] = uint8_t(nvalid);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&ctl->vfull[sv], kTile8);
         __syncwarp();
@@ -542,16 +522,19 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     __syncwarp();
   } else {
     // ------------------------------------------------------------ MMA issuer (warp 5)
-    if (lane == 0) {
+    {
+      const uint32_t leader = elect_one();
+      const uint32_t k_lo0 = sdesc_lo(smem_u32(sK), 16), v_lo0 = sdesc_lo(smem_u32(sV), 0);
+      const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16), p_lo0 = sdesc_lo(smem_u32(sP), 16);
       uint32_t t_glob = 0, n_items = 0;
       int bad = 0;
-      while (!bad && kv8_take<false>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
         const int n = it.n;
         const int R = pad_rows(it.n_q * G);
         const uint32_t idesc_qk = idesc_e4m3_f32(kBN, uint32_t(n_qk(R)), 0, 0);
         const uint32_t idesc_pv = idesc_e4m3_f32(kHeadDim, uint32_t(n_pv(R)), 1, 0);
         const int qb = int(n_items & 1u);
-        const uint32_t q_base = smem_u32(sQ + qb * kQBytes);
+        const uint32_t q_lo = q_lo0 + qb * (kQBytes >> 4);
         if (!mbar_wait(&ctl->q_full[qb], (n_items >> 1) & 1, abort_flag)) { bad = 1; break; }
         tc_fence_after();
         // S^T of tile j of the item into buffer (tile parity)
@@ -560,13 +543,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           const int s = t % kKSt;
           if (!mbar_wait(&ctl->kfull[s], (t / kKSt) & 1, abort_flag)) return false;
           tc_fence_after();
-          const uint32_t k_base = smem_u32(sK + s * kTile8);
+          const uint32_t k_lo = k_lo0 + s * (kTile8 >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_f8(tmem + 32u * (t & 1u), kmajor(k_base, kk), kmajor(q_base, kk), idesc_qk, kk > 0);
-          tc_commit(&ctl->s_full[t & 1]);
-          tc_commit(&ctl->kempty[s]);
-          if (j == n - 1) tc_commit(&ctl->q_empty[qb]);   // the rest of the item reads no Q
+            mma_ss_f8(leader, tmem + 32u * (t & 1u), k_lo + 2 * kk, q_lo + 2 * kk, idesc_qk, kk > 0);
+          tc_commit_by(leader, &ctl->s_full[t & 1]);
+          tc_commit_by(leader, &ctl->kempty[s]);
+          if (j == n - 1) tc_commit_by(leader, &ctl->q_empty[qb]);   // the rest of the item reads no Q
           return true;
         };
         for (int j = 0; j < n && j < 2 && !bad; ++j)
@@ -579,14 +562,13 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (i == 0 && n_items > 0 && !mbar_wait(&ctl->o_free, (n_items - 1) & 1, abort_flag)) { bad = 1; break; }
           if (!mbar_wait(&ctl->p_full[bsel], (t >> 1) & 1, abort_flag)) { bad = 1; break; }
           tc_fence_after();
-          const uint32_t v_base = smem_u32(sV + sv * kTile8);
-          const uint32_t p_base = smem_u32(sP + bsel * kPBytes);
+          const uint32_t v_lo = v_lo0 + sv * (kTile8 >> 4), p_lo = p_lo0 + bsel * (kPBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss_f8(tmem + kColO, vt_desc(v_base, kk), kmajor(p_base, kk), idesc_pv, (i > 0) || (kk > 0));
-          tc_commit(&ctl->pv_done[bsel]);
-          tc_commit(&ctl->vempty[sv]);
-          if (i == n - 1) tc_commit(&ctl->o_full);
+            mma_ss_f8(leader, tmem + kColO, v_lo + kk * (32 * 128 >> 4), p_lo + 2 * kk, idesc_pv, (i > 0) || (kk > 0));
+          tc_commit_by(leader, &ctl->pv_done[bsel]);
+          tc_commit_by(leader, &ctl->vempty[sv]);
+          if (i == n - 1) tc_commit_by(leader, &ctl->o_full);
           if (i + 2 < n && !qk(i + 2)) { bad = 1; break; }
         }
         if (bad) break;
@@ -594,7 +576,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         ++n_items;
       }
       if (bad) raise_abort(ctl, p.err);
-      tc_commit(&ctl->teardown);
+      tc_commit_by(leader, &ctl->teardown);
       wait_quiet(&ctl->teardown, 0);
     }
     __syncwarp();

@@ -19,13 +19,19 @@
 // V enters as fp16 (code * scale, exact for scales that are powers of two):
 // weights in e4m3 would lose what the softmax kept, and splitting them costs
 // the issue-bound softmax warps more than two converting warps cost.
-//   producer warp : per tile 8 + 8 TMA page boxes of 2 KB (K, V), the scales
-//                   (loaded a tile ahead), the mask descriptor
+//   producer warp : per tile 5 + 5 TMA page boxes of 2 KB (K, V), the scales
+//                   (loaded a tile ahead), the mask descriptor; the items
 //   MMA warp      : S_i = Q_i K8^T for both Q tiles, then O_i += P_i V
 //   2 convert warps: V codes -> fp16 in the 128-byte swizzle, slots that hold
 //                   no token zeroed
 //   2 x 4 softmax warps: thread = row = TMEM lane; mask, online max and sum in
-//                   the log2 domain, P (fp16) over the columns of S
+//                   the log2 domain, P (fp16) to columns of its own
+// A tile is 80 keys: then S and P of both Q tiles have tensor-memory columns of
+// their own beside the two O (2 * 80 + 2 * 40 + 2 * 128 = 496 of 512), so that
+// S of the next tile is computed as soon as this one is in registers, under its
+// exponentials. With 128 keys P has to lie over S, and every tile pays the
+// round trip softmax -> PV -> QK -> softmax: 1.9-2.0 us for 128 keys against
+// %s here.
 // Every wait is bounded; a timeout raises a device error instead of hanging.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -38,30 +44,36 @@
 namespace rag {
 namespace f8 {
 
-constexpr int kKSt = 3;                          // K stages (codes)
-constexpr int kRSt = 2;                          // V stages (codes)
-constexpr int kVSt = 2;                          // V stages (fp16)
+constexpr int kPages = kFwdPages;                // pages of a key tile
+constexpr int kKeys = kPages * kPage;            // keys of a tile
+constexpr int kKSt = 4;                          // K stages (codes)
+constexpr int kRSt = 3;                          // V stages (codes)
+constexpr int kVSt = 3;                          // V stages (fp16)
 constexpr int kDescSlots = 4;
-constexpr int kQTileBytes = 2 * kTile8;          // hi and lo
-constexpr int kVTile = kBN * kHeadDim * 2;       // fp16
+constexpr int kPart8 = kBM * kHeadDim;           // hi or lo part of a Q tile
+constexpr int kQTileBytes = 2 * kPart8;
+constexpr int kKTile = kKeys * kHeadDim;         // K or V codes
+constexpr int kVTile = kKeys * kHeadDim * 2;     // fp16
 constexpr int kVHalf = kVTile / 2;               // 64 columns of d
 constexpr int kThreads = 384;                    // 8 softmax + producer, MMA, 2 convert warps
 constexpr float kRescale = 8.0f;                 // log2 units: rescale O when the max grows by > 2^8
 
-// TMEM columns: S_i (P_i aliased over its first 64 columns), O_i
-__host__ __device__ constexpr uint32_t col_s(int qt) { return 128u * qt; }
+// TMEM columns: S_i, P_i (fp16 pairs), O_i
+__host__ __device__ constexpr uint32_t col_s(int qt) { return uint32_t(kKeys) * qt; }
+__host__ __device__ constexpr uint32_t col_p(int qt) { return 2u * kKeys + uint32_t(kKeys / 2) * qt; }
 __host__ __device__ constexpr uint32_t col_o(int qt) { return 256u + 128u * qt; }
+static_assert(col_p(kQTiles) <= 256, "tensor memory");
 
 struct TileDesc {
-  float ks[kPagesPerTile];
-  int32_t lstart[kPagesPerTile];   // logical position of the page's slot 0
-  uint8_t nvalid[kPagesPerTile];
-  int32_t full;                    // every slot of the 8 pages is a token
-  int32_t max_pos;                 // largest logical position of the tile
+  float ks[kPages];
+  int32_t lstart[kPages];   // logical position of the page's slot 0
+  int32_t nvalid[kPages];
+  int32_t full;             // every slot of the pages is a token
+  int32_t max_pos;          // largest logical position of the tile
 };
 struct VInfo {
-  float vs[kPagesPerTile];
-  uint8_t nvalid[kPagesPerTile];
+  float vs[kPages];
+  int32_t nvalid[kPages];
 };
 
 struct Ctrl {
@@ -69,7 +81,7 @@ struct Ctrl {
   uint64_t kfull[kKSt], kempty[kKSt];
   uint64_t rfull[kRSt], rempty[kRSt];
   uint64_t vfull[kVSt], vempty[kVSt];
-  uint64_t s_full[kQTiles], p_lo[kQTiles], p_hi[kQTiles], pv_done[kQTiles], o_full[kQTiles], o_free[kQTiles];
+  uint64_t s_full[kQTiles], s_free[kQTiles], p_full[kQTiles], pv_done[kQTiles], o_full[kQTiles], o_free[kQTiles];
   uint64_t teardown;
   uint64_t desc_full[kDescSlots], desc_empty[kDescSlots];
   TileDesc desc[kDescSlots];
@@ -80,7 +92,7 @@ struct Ctrl {
   int32_t abort;
 };
 
-constexpr size_t kSmemData = size_t(kQTiles) * kQTileBytes + size_t(kKSt + kRSt) * kTile8 + size_t(kVSt) * kVTile;
+constexpr size_t kSmemData = size_t(kQTiles) * kQTileBytes + size_t(kKSt + kRSt) * kKTile + size_t(kVSt) * kVTile;
 constexpr size_t smem_bytes(int num_requests) {
   return 1024 + kSmemData + sizeof(Ctrl) + sizeof(int32_t) * (size_t(num_requests) + 1);
 }
@@ -98,14 +110,30 @@ __device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
   mbar_wait(bar, parity, &zero);
 }
 
-// K-major tile of 128 rows x 128 codes, 128B-swizzled; k-step kk covers codes [32 kk, 32 kk + 32).
-__device__ __forceinline__ uint64_t code_desc(uint32_t base, int kk) { return sdesc_sw128(base + kk * 32, 16, 1024); }
-// V tile [128 keys][128 d] fp16 as the B operand with N = d contiguous: k-step
-// kk covers keys [16 kk, 16 kk + 16); the two 64-wide halves of d are 16 KB
-// apart (leading byte offset), 8-key groups 1 KB apart (stride).
-__device__ __forceinline__ uint64_t v_desc(uint32_t base, int kk) {
-  return sdesc_sw128(base + kk * 16 * 128, kVHalf, 1024);
+// 32 lanes x 16 columns of 32-bit: thread i of the warp gets lane (base + i).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
+// The 40 columns of a tile's P.
+__device__ __forceinline__ void tmem_st_p(uint32_t taddr, const uint32_t (&r)[kKeys / 2]) {
+  static_assert(kKeys / 2 == 40, "16 + 16 + 8 columns");
+  tmem_st16(taddr, r);
+  tmem_st16(taddr + 16, r + 16);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr + 32), "r"(r[32]),
+               "r"(r[33]), "r"(r[34]), "r"(r[35]), "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39])
+               : "memory");
+}
+
+// Low words of the operands' descriptors. Q parts and K tiles are K-major rows
+// of 128 codes: a k-step of 32 codes is 32 bytes on (2 in units of 16). A V tile
+// [80 keys][128 d] fp16 is the B operand with N = d contiguous: a k-step of 16
+// keys is 2 KB on, the two 64-wide halves of d are 10 KB apart (leading offset).
 
 }  // namespace f8
 
@@ -118,8 +146,8 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + kQTiles * kQTileBytes;
-  uint8_t* sR = sK + kKSt * kTile8;
-  uint8_t* sV = sR + kRSt * kTile8;
+  uint8_t* sR = sK + kKSt * kKTile;
+  uint8_t* sV = sR + kRSt * kKTile;
   Ctrl* ctl = reinterpret_cast<Ctrl*>(sV + kVSt * kVTile);
   int32_t* prefix = reinterpret_cast<int32_t*>(ctl + 1);
 
@@ -139,8 +167,8 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     for (int s = 0; s < kVSt; ++s) { mbar_init(&ctl->vfull[s], 2); mbar_init(&ctl->vempty[s], 1); }
     for (int q = 0; q < kQTiles; ++q) {
       mbar_init(&ctl->s_full[q], 1);
-      mbar_init(&ctl->p_lo[q], 128);
-      mbar_init(&ctl->p_hi[q], 128);
+      mbar_init(&ctl->s_free[q], 128);
+      mbar_init(&ctl->p_full[q], 128);
       mbar_init(&ctl->pv_done[q], 1);
       mbar_init(&ctl->o_full[q], 1);
       mbar_init(&ctl->o_free[q], 128);
@@ -177,20 +205,15 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const int r = tid & 127;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const uint32_t o_addr = tmem + lane_off + col_o(qt);
-    uint32_t t_glob = 0;            // tiles seen by the CTA
-    uint32_t n_sf0 = 0, n_sf1 = 0;  // completions of s_full[0] / s_full[1] consumed
-    uint32_t n_pvq = 0;             // PVs into O_qt issued before the current step
-    uint32_t n_of = 0;              // items whose O_qt has been read
+    uint32_t t_glob = 0;   // tiles seen by the CTA
+    uint32_t n_s = 0;      // tiles of this Q tile so far (S read, P written, PV issued)
+    uint32_t n_of = 0;     // items whose O_qt has been read
     int bad = 0;
-    pdl_wait();                     // the row scales come from the kernel before this one
+    pdl_wait();            // the row scales come from the kernel before this one
     while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
       const int n = it.n;
-      // One Q tile: warpgroup 0 alone, alternating between the two S buffers
-      // so that S of the next tile is computed during this tile's softmax.
       const int tok0 = it.rb * p.toks_per_block;
-      const int n_qt = it.n_q - tok0 > TT ? 2 : 1;
-      const bool single = n_qt == 1;
-      const bool active = qt < n_qt;
+      const bool active = qt == 0 || it.n_q - tok0 > TT;   // Q tile 1 may hold no row
       const int tok = tok0 + qt * TT + r / G;
       const int head = it.g * G + r % G;
       const bool row_valid = active && r < TT * G && tok < it.n_q;
@@ -204,77 +227,62 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint32_t slot = t % kDescSlots;
         if (!mbar_wait(&ctl->desc_full[slot], (t / kDescSlots) & 1, abort_flag)) { bad = 1; break; }
         const TileDesc* td = &ctl->desc[slot];
-        float cp[kPagesPerTile];
+        float cp[kPages];
+        int nv[kPages];   // slots of each page that this row sees
+        const int max_pos = td->max_pos;
+        const bool masked = !td->full || max_pos > lim;
 #pragma unroll
-        for (int g = 0; g < kPagesPerTile; ++g) cp[g] = c_row * td->ks[g];
-        // slots of each page that this row sees, a byte a page
-        uint32_t nv_lo = 0x10101010u, nv_hi = 0x10101010u;
-        const bool masked = !td->full || td->max_pos > lim;
+        for (int g = 0; g < kPages; ++g) {
+          cp[g] = c_row * td->ks[g];
+          nv[g] = kPage;
+        }
         if (masked) {
-          nv_lo = *reinterpret_cast<const uint32_t*>(&td->nvalid[0]);
-          nv_hi = *reinterpret_cast<const uint32_t*>(&td->nvalid[4]);
-          if (td->max_pos > lim) {
-            uint32_t a = 0, b = 0;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              a |= uint32_t(min(int((nv_lo >> (8 * g)) & 0xffu), max(lim - td->lstart[g] + 1, 0))) << (8 * g);
-              b |= uint32_t(min(int((nv_hi >> (8 * g)) & 0xffu), max(lim - td->lstart[4 + g] + 1, 0))) << (8 * g);
-            }
-            nv_lo = a;
-            nv_hi = b;
-          }
+          for (int g = 0; g < kPages; ++g) nv[g] = min(td->nvalid[g], lim - td->lstart[g] + 1);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->desc_empty[slot]);
-        if (!active) {
-          // The other warpgroup uses S buffer 1 for the odd tiles; follow its
-          // phases one by one. Descriptors run ahead of the products, and a
-          // parity tells only neighbouring phases apart.
-          if (i & 1) {
-            if (!mbar_wait(&ctl->s_full[1], n_sf1 & 1, abort_flag)) { bad = 1; break; }
-            ++n_sf1;
-          }
-          continue;
-        }
-        const int sb = single ? (i & 1) : qt;   // S buffer of this step
-        const uint32_t s_addr = tmem + lane_off + col_s(sb);
-        if (!mbar_wait(&ctl->s_full[sb], (sb ? n_sf1 : n_sf0) & 1, abort_flag)) { bad = 1; break; }
+        if (!active) continue;
+        const uint32_t s_addr = tmem + lane_off + col_s(qt);
+        if (!mbar_wait(&ctl->s_full[qt], n_s & 1, abort_flag)) { bad = 1; break; }
         tc_fence_after();
         if (!warp_live) {
-          mbar_arrive(&ctl->p_lo[sb]);
-          mbar_arrive(&ctl->p_hi[sb]);
-          if (sb) ++n_sf1; else ++n_sf0;
-          ++n_pvq;
+          // All 32 rows lie past the query block: every arrival, no work. An
+          // arrival for P waits, as the other warps' does, for PV of the tile
+          // before: S of the next tile may be there already, and an arrival
+          // for it must not count for this one.
+          mbar_arrive(&ctl->s_free[qt]);
+          if (i > 0 && !mbar_wait(&ctl->pv_done[qt], (n_s - 1) & 1, abort_flag)) { bad = 1; break; }
+          mbar_arrive(&ctl->p_full[qt]);
+          ++n_s;
           continue;
         }
-        float x[kBN];
+        float x[kKeys];
         {
-          uint32_t u0[32], u1[32], u2[32], u3[32];
+          uint32_t u0[32], u1[32], u2[16];
           tmem_ld32(s_addr + 0, u0);
           tmem_ld32(s_addr + 32, u1);
-          tmem_ld32(s_addr + 64, u2);
-          tmem_ld32(s_addr + 96, u3);
+          tmem_ld16(s_addr + 64, u2);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             x[j] = __uint_as_float(u0[j]);
             x[32 + j] = __uint_as_float(u1[j]);
-            x[64 + j] = __uint_as_float(u2[j]);
-            x[96 + j] = __uint_as_float(u3[j]);
+            if (j < 16) x[64 + j] = __uint_as_float(u2[j]);
           }
         }
+        // S is in registers: the next tile's product may overwrite it
+        tc_fence_before();
+        mbar_arrive(&ctl->s_free[qt]);
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < kBN; ++c) {
-            const int pg = c >> 4;
-            const uint32_t nv = ((pg < 4 ? nv_lo >> (8 * pg) : nv_hi >> (8 * (pg - 4))) & 0xffu);
-            if (uint32_t(c & 15) >= nv) x[c] = -INFINITY;
-          }
+          for (int c = 0; c < kKeys; ++c)
+            if ((c & 15) >= nv[c >> 4]) x[c] = -INFINITY;
         }
         // row max: the largest raw score of each page, scaled by its factor (> 0)
         float mx = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < kPagesPerTile; ++g) {
+        for (int g = 0; g < kPages; ++g) {
           const float* xg = x + 16 * g;
           float a = fmax3(xg[0], xg[1], xg[2]), b = fmax3(xg[3], xg[4], xg[5]);
           a = fmax3(a, xg[6], xg[7]);
@@ -284,6 +292,8 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           a = fmax3(a, xg[14], xg[15]);
           mx = fmaxf(mx, fmaxf(a, b) * cp[g]);
         }
+        // PV of the previous tile has read P (and added to O)
+        if (i > 0 && !mbar_wait(&ctl->pv_done[qt], (n_s - 1) & 1, abort_flag)) { bad = 1; break; }
         float alpha = 1.f;
         bool need = false;
         if (i == 0) {
@@ -293,10 +303,6 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           need = true;
         }
         if (__any_sync(0xffffffffu, need)) {
-          // O must hold the previous tile's PV before it is rescaled. The PV
-          // before that is complete (it was issued ahead of this tile's QK,
-          // whose result is here), so the parity names exactly PV(n_pvq - 1).
-          if (!mbar_wait(&ctl->pv_done[qt], (n_pvq - 1) & 1, abort_flag)) { bad = 1; break; }
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -314,33 +320,25 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const float2 nm2 = make_float2(neg_m, neg_m);
         float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                         make_float2(0.f, 0.f)};
+        uint32_t pk[kKeys / 2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float c = cp[4 * h + (j >> 3)];
-            const float2 y = ffma2(make_float2(x[64 * h + 2 * j], x[64 * h + 2 * j + 1]), make_float2(c, c), nm2);
-            const float2 e = make_float2(ex2(y.x), ex2(y.y));
-            ls[j & 3] = fadd2(ls[j & 3], e);
-            pk[j] = pack_f16x2(e.x, e.y);
-          }
-          tmem_st32(s_addr + 32 * h, pk);   // P over the first 64 columns of S
-          // publish this half of P: PV over its 64 keys may start
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(h == 0 ? &ctl->p_lo[sb] : &ctl->p_hi[sb]);
+        for (int j = 0; j < kKeys / 2; ++j) {
+          const float c = cp[j >> 3];
+          const float2 y = ffma2(make_float2(x[2 * j], x[2 * j + 1]), make_float2(c, c), nm2);
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          ls[j & 3] = fadd2(ls[j & 3], e);
+          pk[j] = pack_f16x2(e.x, e.y);
         }
+        tmem_st_p(tmem + lane_off + col_p(qt), pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&ctl->p_full[qt]);
         const float2 ls01 = fadd2(ls[0], ls[1]), ls23 = fadd2(ls[2], ls[3]);
         l_sum += (ls01.x + ls01.y) + (ls23.x + ls23.y);
-        if (sb) ++n_sf1; else ++n_sf0;
-        ++n_pvq;
+        ++n_s;
       }
       if (bad) break;
       t_glob += n;
-      // completions of s_full[1] that warpgroup 1 consumed in a two-Q-tile item
-      // (all of them by the time O_0 is complete, which comes after the last)
-      if (!single && qt == 0) n_sf1 += uint32_t(n);
       if (!active) continue;
 
       // ---- epilogue: O of this Q tile
@@ -411,73 +409,57 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (!kv8_put(&ctl->ring, n_it++, it, lane, abort_flag)) { bad = 1; break; }
         const int n = it.n;
         const int sub = lane & 7;
-        auto page_id = [&](int tile) {
-          return lane < 16 ? load_page_id(p.batch, walk.req, tile * kPagesPerTile + sub) : -1;
-        };
-        auto resolve = [&](int tile, int32_t id) {
-          PageRef pg;
-          pg.page = -1; pg.nvalid = 0; pg.lstart = 0; pg.chunk = -1;
-          if (lane < 16)
-            pg = page_ref_cached(&ctl->chunks, p.batch, walk.req, tile * kPagesPerTile + sub, id, p.num_pages,
-                                 lane < 8 ? p.err : nullptr);
-          return pg;
-        };
-        // page ids run two tiles ahead, scales one
-        const int32_t first_id = page_id(it.t_begin);
-        int32_t next_id = n > 1 ? page_id(it.t_begin + 1) : -1;
-        if (walk.b != cached_b) {
-          __syncwarp();
-          load_chunk_cache(&ctl->chunks, p.batch, walk.req, lane);
-          cached_b = walk.b;
-        }
-        PageRef pg = resolve(it.t_begin, first_id);
-        float sc = page_scale_load(p, pg, it.g, lane);
+        const bool mine = lane < 16 && sub < kPages;   // a page of K (lanes 0-7) or of V (lanes 8-15)
+        Kv8Pages<kPages> pages;
+        pages.start(p, walk.req, &ctl->chunks, walk.b != cached_b, it.t_begin, it.g, lane);
+        cached_b = walk.b;
         for (int i = 0; i < n; ++i) {
           const uint32_t t = t_glob + i;
-          const int tile = it.t_begin + i;
-          const PageRef cur = pg;
-          const float scale = page_scale_ok(p, sc, lane);
-          if (i + 1 < n) {
-            pg = resolve(tile + 1, next_id);
-            sc = page_scale_load(p, pg, it.g, lane);
-            next_id = i + 2 < n ? page_id(tile + 2) : -1;
-          }
+          const int wi = i % Kv8Pages<kPages>::kTiles;
+          if (wi == 0 && i > 0) pages.advance(p, walk.req, &ctl->chunks, i, it.g, lane);
+          const int from = wi * kPages + (mine ? sub : 0);
+          const int page = __shfl_sync(0xffffffffu, pages.cur.page, from);
+          const int nvalid = __shfl_sync(0xffffffffu, pages.cur.nvalid, from);
+          const int lstart = __shfl_sync(0xffffffffu, pages.cur.lstart, from);
+          const int box = page >= 0 ? ((p.layer * p.num_pages + page) * p.num_kv_heads + it.g) * kPage
+                                    : -kPage;   // fully out of range: the box is zero-filled
+          const int s = t % kKSt;
+          if (t >= uint32_t(kKSt) && !mbar_wait(&ctl->kempty[s], ((t / kKSt) - 1) & 1, abort_flag)) { bad = 1; break; }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->kfull[s], kKTile);
+          __syncwarp();
+          if (mine && lane < 8) tma_load_2d(sK + s * kKTile + sub * kPageBytes8, &tm_k, &ctl->kfull[s], 0, box);
+          ++n_k;
+          // the K boxes need the page alone, what follows its scales
+          if (wi == 0) pages.settle(p);
+          const float ks = __shfl_sync(0xffffffffu, pages.cur_k, from), vs = __shfl_sync(0xffffffffu, pages.cur_v, from);
           const uint32_t slot = t % kDescSlots;
           if (t >= kDescSlots && !mbar_wait(&ctl->desc_empty[slot], ((t / kDescSlots) - 1) & 1, abort_flag)) {
             bad = 1;
             break;
           }
           TileDesc* d = &ctl->desc[slot];
-          const unsigned full_pages = __ballot_sync(0xffffffffu, lane < kPagesPerTile && cur.nvalid == kPage);
-          const int last = lane < kPagesPerTile && cur.nvalid > 0 ? cur.lstart + cur.nvalid - 1 : -1;
+          const unsigned full_pages = __ballot_sync(0xffffffffu, lane < kPages && nvalid == kPage);
+          const int last = lane < kPages && nvalid > 0 ? lstart + nvalid - 1 : -1;
           const int max_pos = __reduce_max_sync(0xffffffffu, last);
-          if (lane < kPagesPerTile) {
-            d->ks[lane] = scale;
-            d->lstart[lane] = cur.lstart;
-            d->nvalid[lane] = uint8_t(cur.nvalid);
+          if (lane < kPages) {
+            d->ks[lane] = ks;
+            d->lstart[lane] = lstart;
+            d->nvalid[lane] = nvalid;
           }
-          if (lane == 0) { d->full = full_pages == 0xffu ? 1 : 0; d->max_pos = max_pos; }
+          if (lane == 0) { d->full = full_pages == (1u << kPages) - 1 ? 1 : 0; d->max_pos = max_pos; }
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->desc_full[slot]);
-          const int box = cur.page >= 0 ? ((p.layer * p.num_pages + cur.page) * p.num_kv_heads + it.g) * kPage
-                                        : -kPage;   // fully out of range: the box is zero-filled
-          const int s = t % kKSt;
-          if (t >= uint32_t(kKSt) && !mbar_wait(&ctl->kempty[s], ((t / kKSt) - 1) & 1, abort_flag)) { bad = 1; break; }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->kfull[s], kTile8);
-          __syncwarp();
-          if (lane < 8) tma_load_2d(sK + s * kTile8 + sub * kPageBytes8, &tm_k, &ctl->kfull[s], 0, box);
-          ++n_k;
           const int sv = t % kRSt;
           if (t >= uint32_t(kRSt) && !mbar_wait(&ctl->rempty[sv], ((t / kRSt) - 1) & 1, abort_flag)) { bad = 1; break; }
-          if (lane >= 8 && lane < 16) {
-            ctl->vinfo[sv].vs[sub] = scale;
-            ctl->vinfo[sv].nvalid[sub] = uint8_t(cur.nvalid);
+          if (mine && lane >= 8) {
+            ctl->vinfo[sv].vs[sub] = vs;
+            ctl->vinfo[sv].nvalid[sub] = nvalid;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&ctl->rfull[sv], kTile8);
+          if (lane == 0) mbar_arrive_expect_tx(&ctl->rfull[sv], kKTile);
           __syncwarp();
-          if (lane >= 8 && lane < 16) tma_load_2d(sR + sv * kTile8 + sub * kPageBytes8, &tm_v, &ctl->rfull[sv], 0, box);
+          if (mine && lane >= 8) tma_load_2d(sR + sv * kKTile + sub * kPageBytes8, &tm_v, &ctl->rfull[sv], 0, box);
           ++n_v;
         }
         t_glob += n;
@@ -497,13 +479,12 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       __syncwarp();
     } else if (warp >= 10) {
       // ------------------------------------------------------------ convert warps
-      // Warp 10 takes keys 0-63, warp 11 keys 64-127. A lane reads 16 codes of
+      // Each warp takes every other group of 4 keys. A lane reads 16 codes of
       // a row and writes two 16-byte vectors of fp16; lanes of the upper half
       // of d write theirs in the other order, so that eight lanes cover all
       // banks with each store. Warp 10 also loads an item's Q tiles, which the
       // kernel before this one makes: the producer warp never waits for it, so
       // K and V stream in while the queries are still being split.
-      const int base_row = (warp - 10) * 64;
       const int c = lane & 7;                         // 16 codes: columns 16c .. 16c + 15
       uint32_t t_glob = 0, q_iter = 0;
       int bad = 0;
@@ -518,7 +499,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_arrive_expect_tx(&ctl->q_full, n_qt * 2 * TT * G * kHeadDim);
             for (int q = 0; q < n_qt; ++q) {
               tma_load_3d(sQ + q * kQTileBytes, &tm_q, &ctl->q_full, 0, it.g * G, it.q0 + tok0 + q * TT);
-              tma_load_3d(sQ + q * kQTileBytes + kTile8, &tm_q, &ctl->q_full, kHeadDim, it.g * G,
+              tma_load_3d(sQ + q * kQTileBytes + kPart8, &tm_q, &ctl->q_full, kHeadDim, it.g * G,
                           it.q0 + tok0 + q * TT);
             }
           }
@@ -530,13 +511,13 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const int sr = t % kRSt, sv = t % kVSt;
           if (!mbar_wait(&ctl->rfull[sr], (t / kRSt) & 1, abort_flag)) { bad = 1; break; }
           if (t >= uint32_t(kVSt) && !mbar_wait(&ctl->vempty[sv], ((t / kVSt) - 1) & 1, abort_flag)) { bad = 1; break; }
-          const uint8_t* src = sR + sr * kTile8;
+          const uint8_t* src = sR + sr * kKTile;
           uint8_t* dst = sV + sv * kVTile + (c >> 2) * kVHalf;
-#pragma unroll 4
-          for (int j = 0; j < 16; ++j) {
-            const int row = base_row + 4 * j + (lane >> 3);
+#pragma unroll 5
+          for (int j = 0; j < kKeys / 8; ++j) {
+            const int row = 8 * j + 4 * (warp - 10) + (lane >> 3);
             const int pgi = row >> 4;
-            const bool live = (row & 15) < int(ctl->vinfo[sr].nvalid[pgi]);
+            const bool live = (row & 15) < ctl->vinfo[sr].nvalid[pgi];
             const __half2 sc = __float2half2_rn(ctl->vinfo[sr].vs[pgi]);
             uint4 u = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
             if (!live) u = make_uint4(0u, 0u, 0u, 0u);
@@ -572,138 +553,77 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       __syncwarp();
     } else {
       // ------------------------------------------------------------ MMA issuer (warp 9)
-      if (lane == 0) {
-        const uint32_t idesc_qk = idesc_e4m3_f32(kBM, kBN, 0, 0);
+      {
+        const uint32_t leader = elect_one();
+        const uint32_t idesc_qk = idesc_e4m3_f32(kBM, kKeys, 0, 0);
         const uint32_t idesc_pv = idesc_f16_f32(kBM, kHeadDim, 1);
-        const uint32_t q_base = smem_u32(sQ);
+        const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16);
+        const uint32_t k_lo0 = sdesc_lo(smem_u32(sK), 16), v_lo0 = sdesc_lo(smem_u32(sV), kVHalf);
         uint32_t t_glob = 0, q_iter = 0;
-        uint32_t n_pf0 = 0, n_pf1 = 0;       // completions of p_lo/p_hi[0] and [1] consumed
+        uint32_t n_s[kQTiles] = {0, 0};      // tiles done, per Q tile
         uint32_t n_item[kQTiles] = {0, 0};   // items begun, per Q tile
         int bad = 0;
-        // S (buffer at column d) = (hi + lo) of the Q tile at qb times K codes at kb
-        auto qk_mma = [&](uint32_t d, uint32_t qb, uint32_t kb) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_ss_f8(tmem + d, code_desc(qb, kk), code_desc(kb, kk), idesc_qk, kk > 0);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss_f8(tmem + d, code_desc(qb + kTile8, kk), code_desc(kb, kk), idesc_qk, 1);
-        };
-        while (!bad && kv8_take<false>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+        while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
           const int n = it.n;
           const int n_qt = it.n_q - it.rb * p.toks_per_block > TT ? 2 : 1;
           if (!mbar_wait(&ctl->q_full, q_iter & 1, abort_flag)) { bad = 1; break; }
           tc_fence_after();
-          if (n_qt == 1) {
-            // One Q tile, two S buffers: QK of tiles 0 and 1 first, then per tile
-            // i, PV(i) as soon as its P is written and QK(i + 2) into the buffer
-            // PV(i) has just read (issue order keeps them apart).
-            auto qk = [&](int j) {
-              const uint32_t t = t_glob + j;
-              const int s = t % kKSt;
-              if (!mbar_wait(&ctl->kfull[s], (t / kKSt) & 1, abort_flag)) return false;
-              tc_fence_after();
-              qk_mma(col_s(j & 1), q_base, smem_u32(sK + s * kTile8));
-              tc_commit(&ctl->s_full[j & 1]);
-              tc_commit(&ctl->kempty[s]);
-              if (j == n - 1) tc_commit(&ctl->q_empty);   // the rest of the item reads no Q
-              return true;
-            };
-            for (int j = 0; j < n && j < 2 && !bad; ++j)
-              if (!qk(j)) bad = 1;
-            for (int i = 0; i < n && !bad; ++i) {
-              const uint32_t t = t_glob + i;
-              const int sv = t % kVSt;
-              const int b = i & 1;
-              if (!mbar_wait(&ctl->vfull[sv], (t / kVSt) & 1, abort_flag)) { bad = 1; break; }
-              if (i == 0) {
-                if (n_item[0] > 0 && !mbar_wait(&ctl->o_free[0], (n_item[0] - 1) & 1, abort_flag)) { bad = 1; break; }
-                ++n_item[0];
-              }
-              uint32_t& npf = b ? n_pf1 : n_pf0;
-              const uint32_t v_base = smem_u32(sV + sv * kVTile);
-              bool ok = true;
-              for (int hh = 0; hh < 2 && ok; ++hh) {
-                if (!mbar_wait(hh == 0 ? &ctl->p_lo[b] : &ctl->p_hi[b], npf & 1, abort_flag)) { ok = false; break; }
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 4 * hh; kk < 4 * hh + 4; ++kk)
-                  mma_ts(tmem + col_o(0), tmem + col_s(b) + kk * 8, v_desc(v_base, kk), idesc_pv, (i > 0) || (kk > 0));
-              }
-              if (!ok) { bad = 1; break; }
-              ++npf;
-              tc_commit(&ctl->pv_done[0]);
-              if (i == n - 1) tc_commit(&ctl->o_full[0]);
-              tc_commit(&ctl->vempty[sv]);
-              if (i + 2 < n && !qk(i + 2)) { bad = 1; break; }
-            }
-            if (bad) break;
-            t_glob += n;
-            ++q_iter;
-            continue;
-          }
-          // Tensor-core order per step: PV_0(t-1), QK_0(t), PV_1(t-1), QK_1(t), so
-          // that softmax 0 of tile t runs while the pipe does PV_1 and QK_1.
-          for (int i = 0; i <= n && !bad; ++i) {
-            const uint32_t t = t_glob + i;          // tile of the QK products of this step
-            const uint32_t tp = t - 1;              // tile of the PV products of this step
+          // S_q = (hi + lo) K^T of tile j for every Q tile, each as soon as the
+          // softmax holds the S before it in registers
+          auto qk = [&](int j) {
+            const uint32_t t = t_glob + j;
             const int s = t % kKSt;
-            const int sv = tp % kVSt;
-            uint32_t v_base = 0;
-            const uint32_t k_base = smem_u32(sK + s * kTile8);
-            if (i >= 1) {
-              if (!mbar_wait(&ctl->vfull[sv], (tp / kVSt) & 1, abort_flag)) { bad = 1; break; }
-              v_base = smem_u32(sV + sv * kVTile);
-            }
-            for (int q = 0; q < kQTiles && !bad; ++q) {
-              if (i >= 1) {
-                // O_q += P_q V for the previous tile
-                if (i == 1) {
-                  if (n_item[q] > 0 && !mbar_wait(&ctl->o_free[q], (n_item[q] - 1) & 1, abort_flag)) {
-                    bad = 1;
-                    break;
-                  }
-                  ++n_item[q];
-                }
-                uint32_t& npf = q ? n_pf1 : n_pf0;
-                bool ok = true;
-                for (int hh = 0; hh < 2 && ok; ++hh) {
-                  if (!mbar_wait(hh == 0 ? &ctl->p_lo[q] : &ctl->p_hi[q], npf & 1, abort_flag)) { ok = false; break; }
-                  tc_fence_after();
+            if (!mbar_wait(&ctl->kfull[s], (t / kKSt) & 1, abort_flag)) return false;
+            const uint32_t k_lo = k_lo0 + s * (kKTile >> 4);
+            for (int q = 0; q < n_qt; ++q) {
+              const uint32_t before = n_s[q] + j;   // S_q read so often by then (j counts from the item's first)
+              if (before > 0 && !mbar_wait(&ctl->s_free[q], (before - 1) & 1, abort_flag)) return false;
+              tc_fence_after();
+              const uint32_t a_lo = q_lo + q * (kQTileBytes >> 4);
 #pragma unroll
-                  for (int kk = 4 * hh; kk < 4 * hh + 4; ++kk)
-                    mma_ts(tmem + col_o(q), tmem + col_s(q) + kk * 8, v_desc(v_base, kk), idesc_pv,
-                           (i > 1) || (kk > 0));
-                }
-                if (!ok) { bad = 1; break; }
-                ++npf;
-                tc_commit(&ctl->pv_done[q]);
-                if (i == n) tc_commit(&ctl->o_full[q]);   // O_q of this item is complete
-                if (q == kQTiles - 1) tc_commit(&ctl->vempty[sv]);   // the last read of this V stage
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss_f8(leader, tmem + col_s(q), a_lo + 2 * kk, k_lo + 2 * kk, idesc_qk, kk > 0);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ss_f8(leader, tmem + col_s(q), a_lo + (kPart8 >> 4) + 2 * kk, k_lo + 2 * kk, idesc_qk, 1);
+              tc_commit_by(leader, &ctl->s_full[q]);
+            }
+            tc_commit_by(leader, &ctl->kempty[s]);
+            if (j == n - 1) tc_commit_by(leader, &ctl->q_empty);   // the rest of the item reads no Q
+            return true;
+          };
+          if (!qk(0)) { bad = 1; break; }
+          for (int i = 0; i < n && !bad; ++i) {
+            const uint32_t t = t_glob + i;
+            const int sv = t % kVSt;
+            if (i + 1 < n && !qk(i + 1)) { bad = 1; break; }
+            if (!mbar_wait(&ctl->vfull[sv], (t / kVSt) & 1, abort_flag)) { bad = 1; break; }
+            const uint32_t v_lo = v_lo0 + sv * (kVTile >> 4);
+            for (int q = 0; q < n_qt; ++q) {
+              if (i == 0) {
+                if (n_item[q] > 0 && !mbar_wait(&ctl->o_free[q], (n_item[q] - 1) & 1, abort_flag)) { bad = 1; break; }
+                ++n_item[q];
               }
-              if (i < n) {
-                // K of this tile is waited for only here, so that PV_0 of the
-                // previous tile never waits on the next tile's load
-                if (q == 0 && !mbar_wait(&ctl->kfull[s], (t / kKSt) & 1, abort_flag)) { bad = 1; break; }
-                // S_q overwrites P_q (aliased over it), which PV_q of the previous
-                // tile reads: tcgen05.mma operations of one CTA execute in issue
-                // order, so no completion wait is needed.
-                tc_fence_after();
-                qk_mma(col_s(q), q_base + q * kQTileBytes, k_base);
-                tc_commit(&ctl->s_full[q]);
-              }
+              if (!mbar_wait(&ctl->p_full[q], (n_s[q] + i) & 1, abort_flag)) { bad = 1; break; }
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                mma_ts_f16(leader, tmem + col_o(q), tmem + col_p(q) + kk * 8, v_lo + kk * (16 * 128 >> 4), idesc_pv,
+                           (i > 0) || (kk > 0));
+              tc_commit_by(leader, &ctl->pv_done[q]);
+              if (i == n - 1) tc_commit_by(leader, &ctl->o_full[q]);
             }
             if (bad) break;
-            if (i < n) tc_commit(&ctl->kempty[s]);
-            // the drain step reads no Q: the next item's Q may load now
-            if (i == n - 1) tc_commit(&ctl->q_empty);
+            tc_commit_by(leader, &ctl->vempty[sv]);
           }
           if (bad) break;
+          for (int q = 0; q < n_qt; ++q) n_s[q] += n;
           t_glob += n;
           ++q_iter;
         }
         if (bad) raise_abort(ctl, p.err);
         // every MMA issued so far completes before TMEM is released
-        tc_commit(&ctl->teardown);
+        tc_commit_by(leader, &ctl->teardown);
         wait_quiet(&ctl->teardown, 0);
       }
       __syncwarp();
@@ -776,16 +696,17 @@ __global__ void __launch_bounds__(256) kv8_split_q_kernel(const Kv8Params p, int
 
 // Merge the partial rows (O, m, l) of every cut unit:
 //   m = max_s m_s, l = sum_s l_s 2^(m_s - m), O = sum_s O_s l_s 2^(m_s - m) / l.
-// Block (c, y) merges rows 32 y .. 32 y + 31 of the unit whose second piece CTA
-// c left (nothing for other CTAs); a warp takes a row at a time, each lane 4 of
-// the 128 columns; lane j holds the statistics of piece s0 + j, and the O
-// slices of kCombineBatch pieces are requested before any is used. (A warp per
-// output row of the batch, each finding its own pieces, took 45 us on 16
-// requests of 32-128 tokens.)
-constexpr int kCombineBatch = 8;
-constexpr int kCombineRows = 32;
-
-__global__ void __launch_bounds__(256, 4) kv8_combine_kernel(const Kv8Params p) {
+// Block (c, y) merges 8 kRowsWarp rows of the unit whose second piece CTA c left
+// (nothing for other CTAs); a warp takes a row at a time, each lane 4 of the 128
+// columns; lane j holds the statistics of piece s0 + j, and the O slices of
+// kBatch pieces are requested before any is used. Stretches leave two or three
+// pieces a unit (4 at a time, two rows a warp, all 64 warps of an SM), pieces
+// up to a dozen (16 at a time, a row a warp). (A warp per output row of the
+// batch, each finding its own pieces, took 45 us on 16 requests of 32-128
+// tokens.)
+template <int kBatch, int kRowsWarp, int kBlocks>
+__global__ void __launch_bounds__(256, kBlocks) kv8_combine_kernel(const Kv8Params p) {
+  constexpr int kRows = 8 * kRowsWarp;
   pdl_launch_dependents();
   pdl_wait();   // partials and cuts come from the attention kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -797,7 +718,7 @@ __global__ void __launch_bounds__(256, 4) kv8_combine_kernel(const Kv8Params p) 
   const int TT = p.decode ? p.toks_per_block : p.toks_per_block / kQTiles;   // tokens of a Q tile
   const int n_piece = c1 - c0 + 1;
   const size_t slot = size_t(p.item_rows) * kPartStride;
-  for (int rr = blockIdx.y * kCombineRows + warp; rr < min(p.item_rows, int(blockIdx.y + 1) * kCombineRows); rr += 8) {
+  for (int rr = blockIdx.y * kRows + warp; rr < min(p.item_rows, int(blockIdx.y + 1) * kRows); rr += 8) {
     const int r = rr % kBM, tok = rr / kBM * TT + r / G;
     if (r >= TT * G || tok >= n_tok) continue;   // uniform over the warp
     const float* row0 = p.part + size_t(2 * c0) * slot + size_t(rr) * kPartStride;
@@ -805,13 +726,13 @@ __global__ void __launch_bounds__(256, 4) kv8_combine_kernel(const Kv8Params p) 
     constexpr int kStatOff = kHeadDim / 2;   // 32-bit word of m (then l) in a row
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < n_piece; s0 += kCombineBatch) {
-      const float2 ml = (lane < kCombineBatch && s0 + lane < n_piece)
+    for (int s0 = 0; s0 < n_piece; s0 += kBatch) {
+      const float2 ml = (lane < kBatch && s0 + lane < n_piece)
                             ? __ldcg(reinterpret_cast<const float2*>(piece(s0 + lane) + kStatOff))
                             : make_float2(-INFINITY, 0.f);
-      uint2 v[kCombineBatch];
+      uint2 v[kBatch];
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j)
+      for (int j = 0; j < kBatch; ++j)
         v[j] = s0 + j < n_piece ? __ldcg(reinterpret_cast<const uint2*>(piece(s0 + j)) + lane) : make_uint2(0u, 0u);
       float mb = fmaxf(m, ml.x);
       for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
@@ -824,7 +745,7 @@ __global__ void __launch_bounds__(256, 4) kv8_combine_kernel(const Kv8Params p) 
       m = mb;
       const float wl = (ml.x == -INFINITY) ? ml.y : ml.y * ex2(ml.x - mu);   // l = 0 there, or nan
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         const float wgt = __shfl_sync(0xffffffffu, wl, j);
         const float2 lo = f16x2_to_f32x2(v[j].x), hi = f16x2_to_f32x2(v[j].y);
         l += wgt;
@@ -859,8 +780,9 @@ cudaError_t launch_kv8_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const C
 }
 
 cudaError_t launch_kv8_combine(const Kv8Params& p, cudaStream_t stream) {
-  return launch_pdl(kv8_combine_kernel, dim3(p.grid, (p.item_rows + kCombineRows - 1) / kCombineRows), dim3(256), 0,
-                    stream, 1, p);
+  if (p.split_tiles > 0)
+    return launch_pdl(kv8_combine_kernel<16, 1, 4>, dim3(p.grid, p.item_rows / 8), dim3(256), 0, stream, 1, p);
+  return launch_pdl(kv8_combine_kernel<4, 2, 8>, dim3(p.grid, p.item_rows / 16), dim3(256), 0, stream, 1, p);
 }
 
 }  // namespace rag
