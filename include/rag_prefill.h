@@ -483,7 +483,9 @@ RAG_API size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch*
  * power-of-two scale per row (together at least the 8 bits of a bf16 value down
  * to 2^-14 of the row's largest, 2^-18 of it absolute), K as its codes, with
  * fp32 sums; the softmax runs in fp32; the weights enter the second product in
- * at least 11 bits, V exactly, with fp32 sums.
+ * at least 11 bits (those below 2^-14 of the row's largest with an error of at
+ * most 2^-24 of it), V exactly, with fp32 sums. A nan or an infinity in a query
+ * makes that row nan.
  * The workspace's error word collects page, geometry and timeout errors as
  * rag_fused_prefill_attn's, and RAG_ERR_RANGE for a scale outside the range
  * above (it is taken as 1). */

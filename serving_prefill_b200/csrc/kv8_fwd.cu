@@ -568,53 +568,62 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           const int n_qt = it.n_q - it.rb * p.toks_per_block > TT ? 2 : 1;
           if (!mbar_wait(&ctl->q_full, q_iter & 1, abort_flag)) { bad = 1; break; }
           tc_fence_after();
-          // S_q = (hi + lo) K^T of tile j for every Q tile, each as soon as the
-          // softmax holds the S before it in registers
-          auto qk = [&](int j) {
+          const bool two = n_qt == 2;
+          // S_q = (hi + lo) K^T of tile j, once the softmax holds the S before
+          // it in registers
+          auto qk = [&](int q, int j) {
             const uint32_t t = t_glob + j;
             const int s = t % kKSt;
             if (!mbar_wait(&ctl->kfull[s], (t / kKSt) & 1, abort_flag)) return false;
-            const uint32_t k_lo = k_lo0 + s * (kKTile >> 4);
-            for (int q = 0; q < n_qt; ++q) {
-              const uint32_t before = n_s[q] + j;   // S_q read so often by then (j counts from the item's first)
-              if (before > 0 && !mbar_wait(&ctl->s_free[q], (before - 1) & 1, abort_flag)) return false;
-              tc_fence_after();
-              const uint32_t a_lo = q_lo + q * (kQTileBytes >> 4);
+            const uint32_t before = n_s[q] + j;   // reads of S_q by then
+            if (before > 0 && !mbar_wait(&ctl->s_free[q], (before - 1) & 1, abort_flag)) return false;
+            tc_fence_after();
+            const uint32_t k_lo = k_lo0 + s * (kKTile >> 4), a_lo = q_lo + q * (kQTileBytes >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss_f8(leader, tmem + col_s(q), a_lo + 2 * kk, k_lo + 2 * kk, idesc_qk, kk > 0);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss_f8(leader, tmem + col_s(q), a_lo + 2 * kk, k_lo + 2 * kk, idesc_qk, kk > 0);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss_f8(leader, tmem + col_s(q), a_lo + (kPart8 >> 4) + 2 * kk, k_lo + 2 * kk, idesc_qk, 1);
-              tc_commit_by(leader, &ctl->s_full[q]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ss_f8(leader, tmem + col_s(q), a_lo + (kPart8 >> 4) + 2 * kk, k_lo + 2 * kk, idesc_qk, 1);
+            tc_commit_by(leader, &ctl->s_full[q]);
+            if (q == n_qt - 1) {                  // the last read of this K stage
+              tc_commit_by(leader, &ctl->kempty[s]);
+              if (j == n - 1) tc_commit_by(leader, &ctl->q_empty);   // the rest of the item reads no Q
             }
-            tc_commit_by(leader, &ctl->kempty[s]);
-            if (j == n - 1) tc_commit_by(leader, &ctl->q_empty);   // the rest of the item reads no Q
             return true;
           };
-          if (!qk(0)) { bad = 1; break; }
-          for (int i = 0; i < n && !bad; ++i) {
-            const uint32_t t = t_glob + i;
+          // O_q += P_q V of tile j
+          auto pv = [&](int q, int j) {
+            const uint32_t t = t_glob + j;
             const int sv = t % kVSt;
-            if (i + 1 < n && !qk(i + 1)) { bad = 1; break; }
-            if (!mbar_wait(&ctl->vfull[sv], (t / kVSt) & 1, abort_flag)) { bad = 1; break; }
-            const uint32_t v_lo = v_lo0 + sv * (kVTile >> 4);
-            for (int q = 0; q < n_qt; ++q) {
-              if (i == 0) {
-                if (n_item[q] > 0 && !mbar_wait(&ctl->o_free[q], (n_item[q] - 1) & 1, abort_flag)) { bad = 1; break; }
-                ++n_item[q];
-              }
-              if (!mbar_wait(&ctl->p_full[q], (n_s[q] + i) & 1, abort_flag)) { bad = 1; break; }
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                mma_ts_f16(leader, tmem + col_o(q), tmem + col_p(q) + kk * 8, v_lo + kk * (16 * 128 >> 4), idesc_pv,
-                           (i > 0) || (kk > 0));
-              tc_commit_by(leader, &ctl->pv_done[q]);
-              if (i == n - 1) tc_commit_by(leader, &ctl->o_full[q]);
+            if (!mbar_wait(&ctl->vfull[sv], (t / kVSt) & 1, abort_flag)) return false;
+            if (j == 0) {
+              if (n_item[q] > 0 && !mbar_wait(&ctl->o_free[q], (n_item[q] - 1) & 1, abort_flag)) return false;
+              ++n_item[q];
             }
-            if (bad) break;
-            tc_commit_by(leader, &ctl->vempty[sv]);
+            if (!mbar_wait(&ctl->p_full[q], (n_s[q] + j) & 1, abort_flag)) return false;
+            tc_fence_after();
+            const uint32_t v_lo = v_lo0 + sv * (kVTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma_ts_f16(leader, tmem + col_o(q), tmem + col_p(q) + kk * 8, v_lo + kk * (16 * 128 >> 4), idesc_pv,
+                         (j > 0) || (kk > 0));
+            tc_commit_by(leader, &ctl->pv_done[q]);
+            if (j == n - 1) tc_commit_by(leader, &ctl->o_full[q]);
+            if (q == n_qt - 1) tc_commit_by(leader, &ctl->vempty[sv]);   // the last read of this V stage
+            return true;
+          };
+          // Q tile 1 follows Q tile 0 by about half a tile: its PV waits for Q
+          // tile 0's next S, so that one warpgroup's exponentials run while the
+          // other one's S and O are made. (Issued tile by tile for both, the
+          // warpgroups run in step and share the exponential unit: 532 against
+          // %s us on the 70B-shaped prompt.)
+          if (!qk(0, 0)) bad = 1;
+          for (int i = 0; i <= n && !bad; ++i) {
+            if (two && i < n && !qk(1, i)) { bad = 1; break; }
+            if (i + 1 < n && !qk(0, i + 1)) { bad = 1; break; }
+            if (two && i > 0 && !pv(1, i - 1)) { bad = 1; break; }
+            if (i < n && !pv(0, i)) { bad = 1; break; }
           }
           if (bad) break;
           for (int q = 0; q < n_qt; ++q) n_s[q] += n;

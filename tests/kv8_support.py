@@ -89,7 +89,10 @@ class AttnCase:
 def reference(dense, q_lens, q, H, G, causal, scale):
     """fp64 O, lse and the bounds of their errors. The bounds count, per row:
     the output's bf16 half step (2^-8 of the value); the weights' and a split
-    row's fp16 half steps (2^-11 each) against sum alpha |v|; and the scores'
+    row's fp16 half steps (2^-11 each) against sum alpha |v|, where a weight
+    below 2^-14 of the row's largest has fp16's subnormal half step, 2^-25 of
+    that largest (whose share of the row is at most 1): 2^-25 sum |v| more; an
+    output below fp16's normal range likewise 2^-24; and the scores'
     error d as a relative error of the weights (2 d): queries in two e4m3 parts
     are off by at most 2^-10 of a row scale that is below max|q| / 224, and
     fp32 sums of 256 products by 256 * 2^-24 of the sum of magnitudes."""
@@ -117,7 +120,8 @@ def reference(dense, q_lens, q, H, G, causal, scale):
             rel = 2 * 2.0 ** -11 + 2 * d + 2.0 ** -14
             O.append(o.reshape(H * G, 128))
             L.append(torch.logsumexp(s, -1).reshape(-1))
-            bo.append((2.0 ** -8 * o.abs() + rel[..., None] * av + 2.0 ** -24).reshape(H * G, 128))
+            floor = 2.0 ** -25 * vv.abs().sum(0)[:, None]
+            bo.append((2.0 ** -8 * o.abs() + rel[..., None] * av + floor + 2.0 ** -24).reshape(H * G, 128))
             bl.append((d + 2.0 ** -14 + 2.0 ** -22 * s.abs().amax(-1)).reshape(-1))
         q0 += nq
     z = lambda xs, *sh: torch.stack(xs) if xs else torch.zeros(0, *sh, dtype=torch.float64)  # noqa: E731

@@ -103,3 +103,73 @@ def test_binding_checks_shapes_types_and_strides():
         sp.rag_kv8_append(pool, 0, s, k, k, rope=torch.zeros(5, 32, 2))       # a table of another head_dim
     with pytest.raises(AssertionError):
         sp.KV8Pool(1, 4, 2, device="cpu", k=torch.zeros(1, 4, 2, 16, 128))
+
+
+# ---------------------------------------------------------------- attention over the 8-bit pool
+
+from serving_prefill_b200.rag import RagBatch  # noqa: E402
+
+WORKSPACE = 7
+
+
+def batch(B=2, q=(10, 20), docs=(100, 50)):
+    pages = [-(-d // 16) for d in docs]
+    return RagBatch(B, B, sum(pages), sum(q), sum(docs), max(q), max(docs), max(pages),
+                    0x30000, 0x31000, 0x32000, 0x33000, 0x34000)
+
+
+def attend(pool, b, hq=32, layer=0, q=0x40000, o=0x70000, lse=None, ws=0x80000, ws_bytes=1 << 40, scale=0.0, causal=1):
+    return lib().rag_kv8_attn(ctypes.byref(pool), layer, ctypes.byref(b) if b is not None else None, q, hq, scale,
+                              causal, o, lse, ws, ws_bytes, None)
+
+
+def test_attention_refuses_before_a_launch():
+    assert attend(pool8(), None) == INVALID
+    for bad in (dict(layer=-1), dict(layer=2), dict(q=None), dict(o=None), dict(q=0x40008), dict(o=0x70004),
+                dict(lse=0x90002), dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert attend(pool8(), batch(), **bad) == INVALID, bad
+    assert attend(pool8(), batch(), hq=30) == SHAPE
+    assert attend(pool8(), batch(), hq=0) == SHAPE
+    assert attend(pool8(), batch(), hq=8 * 129) == UNSUPPORTED       # more than 128 query heads a KV head
+    assert attend(pool8(head_dim=64), batch()) == UNSUPPORTED
+    assert attend(pool8(page=8), batch()) == UNSUPPORTED
+    for bad in (dict(ws=None), dict(ws=0x80080), dict(ws_bytes=4096)):
+        assert attend(pool8(), batch(), **bad) == WORKSPACE, bad
+    many = batch()
+    many.num_requests = 4097
+    assert attend(pool8(), many) == UNSUPPORTED
+    over = batch()
+    over.max_q = 31                                                   # above the total
+    assert attend(pool8(), over) == SHAPE
+    huge = batch(q=(1 << 24, 1 << 24), docs=(1 << 24, 1 << 24))       # weights past 31 bits
+    assert attend(pool8(), huge) == UNSUPPORTED
+
+
+def test_attention_of_no_queries_does_nothing():
+    assert attend(pool8(), batch(B=0, q=(0, 0), docs=(0, 0)), q=None, o=None) == 0
+    assert attend(pool8(), batch(q=(0, 0)), q=None, o=None) == 0
+
+
+def test_attention_workspace_size():
+    size = lambda b, hq=32: lib().rag_kv8_workspace_size(ctypes.byref(pool8()), ctypes.byref(b), hq)  # noqa: E731
+    assert size(batch(), hq=30) == 0 and size(batch(), hq=8 * 129) == 0
+    assert 256 <= size(batch(q=(1, 1), docs=(30, 20))) <= 4096         # short requests: no partial rows
+    assert size(batch(q=(1, 1), docs=(3000, 2000))) < size(batch(q=(100, 100), docs=(3000, 2000)))
+    need = size(batch(docs=(3000, 2000)))
+    assert attend(pool8(), batch(docs=(3000, 2000)), ws_bytes=need - 1) == WORKSPACE
+
+
+def test_attention_binding_checks():
+    pool = sp.KV8Pool(1, 8, 2, device="cpu")
+    b = sp.Batch([0, 1], [0, 40], [0, 3], [1, 2, 3], [0, 4], device="cpu")
+    q, ws = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(1 << 20, dtype=torch.uint8)
+    o = torch.empty_like(q)
+    for bad in (q[:3], q[:, :, :64], q.float(), q[0], torch.zeros(4, 128, 8, dtype=torch.bfloat16).transpose(1, 2)):
+        with pytest.raises(sp.RagError):
+            sp.rag_kv8_attn(pool, 0, b, bad, o, ws)
+    for bad in (o[:3], o.float()):
+        with pytest.raises(sp.RagError):
+            sp.rag_kv8_attn(pool, 0, b, q, bad, ws)
+    for lse in (torch.zeros(4, 7), torch.zeros(4, 8, dtype=torch.bfloat16)):
+        with pytest.raises(sp.RagError):
+            sp.rag_kv8_attn(pool, 0, b, q, o, ws, row_lse=lse)
