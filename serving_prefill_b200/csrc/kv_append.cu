@@ -133,13 +133,15 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
 
 // Two pairs turned at once (x of a and b: one pair, y: the next): a c - b s and
 // b c + a s, every product and sum rounded on its own, which is part of the
-// operator (see above). x - y is the fused x + y * -1: that product is exact.
+// operator (see above). The scalar intrinsics are never contracted; packed
+// products followed by packed sums were fused on their way to the machine.
 __device__ __forceinline__ void turn2(float2& a, float2& b, float4 cs) {   // cs: both cosines, both sines
-  const float2 c = make_float2(cs.x, cs.y), sn = make_float2(cs.z, cs.w);
-  const float2 na = ffma2(fmul2(b, sn), make_float2(-1.f, -1.f), fmul2(a, c));
-  const float2 nb = fadd2(fmul2(b, c), fmul2(a, sn));
-  a = na;
-  b = nb;
+  const float ax = __fsub_rn(__fmul_rn(a.x, cs.x), __fmul_rn(b.x, cs.z));
+  const float ay = __fsub_rn(__fmul_rn(a.y, cs.y), __fmul_rn(b.y, cs.w));
+  b.x = __fadd_rn(__fmul_rn(b.x, cs.x), __fmul_rn(a.x, cs.z));
+  b.y = __fadd_rn(__fmul_rn(b.y, cs.y), __fmul_rn(a.y, cs.w));
+  a.x = ax;
+  a.y = ay;
 }
 
 // A table row in shared memory: the vector (two pairs) that lane c of a row

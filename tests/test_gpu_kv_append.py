@@ -181,16 +181,19 @@ def test_head_layouts_without_rotation(kind, H, G):
         check_q(case)
 
 
-@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32", "f32_64"])
 def test_bits_are_the_fp32_formulas(kind):
     """Rotation in fp32 with each product and sum rounded, one rounding to the
     stored type: the same bits from numpy's fp32."""
-    case = Case(kind, [0, 9], [40, 30], seed=3)
+    case = Case(kind, [0, 9], [400, 300], seed=3)
     before = case.state()
     case.run()
     after = case.state()
-    _, k, v = case.host
+    q, k, v = case.host
     pos = case.positions()
+    if kind.startswith("f32"):
+        q32 = np.stack([oa.rotate(q[t].astype(np.float32), case.table[pos[t]]) for t in range(case.T)])
+        np.testing.assert_array_equal(case.q_out[:case.T].cpu().numpy(), q32)
     k32 = np.stack([oa.rotate(k[t].astype(np.float32), case.table[pos[t]]) for t in range(case.T)])
     assert k32.dtype == np.float32
     want = [None if x is None else x.copy() for x in before]
@@ -201,7 +204,7 @@ def test_bits_are_the_fp32_formulas(kind):
         np.testing.assert_array_equal(after[0], oa.to_e4m3(want[0]))
         np.testing.assert_array_equal(after[1], oa.to_e4m3(want[1]))
     else:
-        np.testing.assert_array_equal(after[0], torch.from_numpy(want[0]).float().to(torch.bfloat16).double().numpy())
+        np.testing.assert_array_equal(after[0], torch.from_numpy(want[0]).float().to(case.dt).double().numpy())
 
 
 def test_scale_grows_token_by_token_and_held_codes_follow():
