@@ -217,7 +217,7 @@ struct Kv8Item {
 struct Kv8Ring {
   uint64_t full[kItemSlots], empty[kItemSlots];
   Kv8Item item[kItemSlots];
-  int32_t total, ctas, pieces;   // the line: weight, CTAs that share it, 1: measured in pieces
+  int32_t total, stretch, pieces;   // the line: weight, a CTA's share of it, 1: measured in pieces
   ReqInfo req[kReqCache];
 };
 
@@ -254,7 +254,7 @@ __device__ __forceinline__ ReqInfo kv8_req(const Kv8Params& p, const Kv8Ring* ri
 }
 
 // The line of the batch (one warp): each request's weight as an exclusive
-// prefix, the total, the CTAs that share it.
+// prefix, the total, a CTA's stretch.
 __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv8Ring* ring, int lane) {
   const int B = p.batch.num_requests;
   const bool one_piece_each = p.part != nullptr;   // cut units: one piece a CTA
@@ -292,10 +292,9 @@ __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv
   }
   if (lane == 0) {
     const int W = int(carry);
-    const int most = pieces ? W : W / (p.decode ? kMinWorkDecode : kMinWork);
     prefix[B] = W;
     ring->total = W;
-    ring->ctas = max(1, min(most, p.grid));
+    ring->stretch = max(int((uint32_t(W) + p.grid - 1) / p.grid), pieces ? 1 : p.decode ? kMinWorkDecode : kMinWork);
     ring->pieces = pieces ? 1 : 0;
   }
   __syncwarp();
@@ -308,14 +307,14 @@ struct Kv8Walk {
   Kv8Cut cut;
 
   __device__ __forceinline__ void start(const Kv8Ring* ring) {
-    const int W = ring->total, C = ring->ctas, c = int(blockIdx.x);
+    const uint32_t W = ring->total, L = ring->stretch, c = blockIdx.x;
     pos = end = 0;
     b = -1;
     per_head = 1;
     cut = {};
-    if (W == 0 || c >= C) return;
-    pos = int(int64_t(c) * W / C);
-    end = int(int64_t(c + 1) * W / C);
+    if (c * uint64_t(L) >= W) return;
+    pos = int(c * L);
+    end = int(min(W, c * L + L));
   }
   __device__ __forceinline__ bool next(const Kv8Params& p, const int32_t* prefix, const Kv8Ring* ring, Kv8Item& it) {
     const bool pieces = ring->pieces != 0;
@@ -342,8 +341,9 @@ struct Kv8Walk {
       const int s = pos - rem, n = kv8_tiles(p, req, it.rb), cost = kv8_cost(p, req, it.rb);
       int t_begin, t_end;
       if (pieces) {
-        t_begin = int(int64_t(rem) * n / w);
-        t_end = int(int64_t(rem + 1) * n / w);
+        const int q = n / w, r = n % w;           // piece i: q tiles, the first r pieces one more
+        t_begin = rem * q + min(rem, r);
+        t_end = t_begin + q + (rem < r ? 1 : 0);
         pos += 1;
       } else {
         t_begin = ceil_div(rem, cost);
@@ -360,15 +360,14 @@ struct Kv8Walk {
       it.n_doc = req.n_doc;
       if (t_begin > 0) {
         // a piece that goes on from another CTA's: the second of its unit reports the cut
-        const int64_t W = ring->total, C = ring->ctas;
-        const int c0 = int((int64_t(s + 1) * C - 1) / W);
-        const int last = pieces ? s + w - 1 : s + (n - 1) * cost;   // the last piece, or tile, begins here
-        if (cta == c0 + 1) {
+        const uint32_t L = ring->stretch, c0 = uint32_t(s) / L;
+        if (cta == int(c0) + 1) {
+          const int last = pieces ? s + w - 1 : s + (n - 1) * cost;   // the last piece, or tile, begins here
           cut.n_tok = min(p.toks_per_block, req.n_q - it.rb * p.toks_per_block);
           cut.tok0 = req.q0 + it.rb * p.toks_per_block;
           cut.head0 = it.g * p.group;
-          cut.c0 = c0;
-          cut.c1 = int((int64_t(last + 1) * C - 1) / W);
+          cut.c0 = int(c0);
+          cut.c1 = int(uint32_t(last) / L);
         }
       }
       return true;
@@ -415,7 +414,7 @@ __device__ __forceinline__ bool kv8_take(Kv8Ring* ring, uint32_t j, Kv8Item& it,
 template <int kPagesTile>
 struct Kv8Pages {
   static constexpr int kTiles = 32 / kPagesTile;
-  int base, next_id;          // first page reference of the item; id of this lane's page two windows on
+  int base, next_id;          // first page reference of the item; id of this lane's page in the next window to resolve
   PageRef cur, nxt;
   float cur_k, cur_v, nxt_k, nxt_v;
 
@@ -443,30 +442,32 @@ struct Kv8Pages {
     if (!(cur_k > 0.f && cur_k < INFINITY)) { atomicOr(p.err, kDevErrRange); cur_k = 1.f; }
     if (!(cur_v > 0.f && cur_v <= 128.f)) { atomicOr(p.err, kDevErrRange); cur_v = 1.f; }
   }
+  // The first window; the next one's ids are on their way.
   __device__ __forceinline__ void start(const Kv8Params& p, const ReqInfo& r, ChunkCache* cc, bool load_chunks,
                                         int t_begin, int g, int lane) {
     base = t_begin * kPagesTile;
-    const int id0 = id(p, r, 0, lane), id1 = id(p, r, 1, lane);
-    next_id = id(p, r, 2, lane);
+    const int id0 = id(p, r, 0, lane);
+    next_id = id(p, r, 1, lane);
     if (load_chunks) {
       __syncwarp();
       load_chunk_cache(cc, p.batch, r, lane);
     }
     cur = resolve(p, r, cc, 0, id0, lane);
     scales(p, cur, g, cur_k, cur_v);
-    nxt = resolve(p, r, cc, 1, id1, lane);
-    scales(p, nxt, g, nxt_k, nxt_v);
   }
-  // tile i of the item begins a window (i > 0)
-  __device__ __forceinline__ void advance(const Kv8Params& p, const ReqInfo& r, const ChunkCache* cc, int i, int g,
-                                          int lane) {
+  // Once the boxes of the first tile of a window are under way: the window after it.
+  __device__ __forceinline__ void ahead(const Kv8Params& p, const ReqInfo& r, const ChunkCache* cc, int i, int g,
+                                        int lane) {
     const int w = i / kTiles;
-    cur = nxt;
-    cur_k = nxt_k;
-    cur_v = nxt_v;
     nxt = resolve(p, r, cc, w + 1, next_id, lane);
     scales(p, nxt, g, nxt_k, nxt_v);
     next_id = id(p, r, w + 2, lane);
+  }
+  // The first tile of a later window.
+  __device__ __forceinline__ void advance() {
+    cur = nxt;
+    cur_k = nxt_k;
+    cur_v = nxt_v;
   }
 };
 

@@ -370,7 +370,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       for (int i = 0; i < n; ++i) {
         const uint32_t t = t_glob + i;
         const int wi = i % Kv8Pages<kPagesPerTile>::kTiles;
-        if (wi == 0 && i > 0) pages.advance(p, walk.req, &ctl->chunks, i, it.g, lane);
+        if (wi == 0 && i > 0) pages.advance();
         const int from = wi * kPagesPerTile + sub;
         const int page = __shfl_sync(0xffffffffu, pages.cur.page, from);
         const int nvalid = __shfl_sync(0xffffffffu, pages.cur.nvalid, from);
@@ -411,6 +411,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         __syncwarp();
         if (lane >= 8 && lane < 16) tma_load_2d(sV + sv * kTile8 + sub * kPageBytes8, &tm_v, &ctl->vfull[sv], 0, box);
         ++n_v;
+        if (wi == 0) pages.ahead(p, walk.req, &ctl->chunks, i, it.g, lane);
       }
       t_glob += n;
     }

@@ -416,7 +416,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int i = 0; i < n; ++i) {
           const uint32_t t = t_glob + i;
           const int wi = i % Kv8Pages<kPages>::kTiles;
-          if (wi == 0 && i > 0) pages.advance(p, walk.req, &ctl->chunks, i, it.g, lane);
+          if (wi == 0 && i > 0) pages.advance();
           const int from = wi * kPages + (mine ? sub : 0);
           const int page = __shfl_sync(0xffffffffu, pages.cur.page, from);
           const int nvalid = __shfl_sync(0xffffffffu, pages.cur.nvalid, from);
@@ -461,6 +461,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           __syncwarp();
           if (mine && lane >= 8) tma_load_2d(sR + sv * kKTile + sub * kPageBytes8, &tm_v, &ctl->rfull[sv], 0, box);
           ++n_v;
+          if (wi == 0) pages.ahead(p, walk.req, &ctl->chunks, i, it.g, lane);
         }
         t_glob += n;
       }

@@ -199,7 +199,7 @@ template <> struct Vec<float> {
 // where it goes: the first kAhead rows of every group are requested before the
 // tokens are resolved (a warp a token) and arrive under that chain of
 // dependent loads.
-constexpr int kAhead = 3;
+constexpr int kAhead = 2;
 
 template <typename T, int kDim, bool kKV>
 __device__ __forceinline__ void store_rows(const AppendParams& p, Tok* toks, float4* tab, int t0, int tpb) {
@@ -758,6 +758,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
   uint8_t* smem = smem_raw + ((16 - (smem_u32(smem_raw) & 15)) & 15);
   float4* tabs = reinterpret_cast<float4*>(smem + kStreamStages * kStageBytes);
   StreamCtrl* ctl = reinterpret_cast<StreamCtrl*>(tabs + kStreamStages * kStageTab);
+  if (p.q) pdl_launch_dependents();   // the queries' kernel, which waits for this one at its end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < kStreamStages; ++s) {
@@ -858,11 +859,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
   if (err && p.err) atomicOr(p.err, err);
 }
 
-// Queries alone, beside the streamed cache blocks of a call with many tokens.
-__global__ void __launch_bounds__(kAppendThreads, 3) rope_q_kernel(const AppendParams p) {
+// Queries alone, beside the streamed cache blocks of a call with many tokens:
+// the stream kernel releases this one as soon as its blocks have started, and
+// this one completes only after it, so that whatever follows finds both done.
+__global__ void __launch_bounds__(kAppendThreads, 4) rope_q_kernel(const AppendParams p) {
   __shared__ Tok toks[kMaxTokensPerBlock];
   __shared__ float4 tab[kMaxTokensPerBlock * 32];
   store_rows<__nv_bfloat16, kHeadDim, false>(p, toks, tab, int(blockIdx.x) * p.tokens_per_block, p.tokens_per_block);
+  pdl_wait();
 }
 
 // (cos, sin) of position p and pair i: the angle p * base^(-2 i / d), in fp64,
@@ -877,8 +881,9 @@ __global__ void __launch_bounds__(256) rope_cos_sin_kernel(double base, int half
 }
 
 // The kernels below write pool pages and queries that the next kernel may read
-// before its own wait, so they release no dependents early and start only once
-// the kernel before them has completed.
+// before its own wait, so they release no dependents early (the stream kernel
+// only the queries' kernel of its own call) and start only once the kernel
+// before them has completed.
 cudaError_t launch_kv_append(const AppendParams& p, int is_f32, int grid, cudaStream_t stream) {
   const auto kernel = !is_f32               ? kv_append_kernel<__nv_bfloat16, 128>
                       : p.head_dim == 128 ? kv_append_kernel<float, 128>
@@ -895,7 +900,7 @@ cudaError_t launch_kv8_append_stream(const AppendParams& p, int grid, cudaStream
   return launch_plain(kv8_append_stream_kernel, dim3(grid), dim3(kStreamThreads), kStreamSmem, stream, p);
 }
 cudaError_t launch_rope_q(const AppendParams& p, int grid, cudaStream_t stream) {
-  return launch_plain(rope_q_kernel, dim3(grid), dim3(kAppendThreads), 0, stream, p);
+  return launch_pdl(rope_q_kernel, dim3(grid), dim3(kAppendThreads), 0, stream, 1, p);
 }
 cudaError_t launch_rope_cos_sin(double base, int head_dim, int n_pos, float2* table, cudaStream_t stream) {
   const int64_t n = int64_t(n_pos) * (head_dim / 2);

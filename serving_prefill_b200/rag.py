@@ -379,11 +379,14 @@ def rag_rope_cos_sin(base: float, head_dim: int, n_pos: int, device="cuda", stre
 
 def _row_stride(t, rows, heads, dim, dtype, dev, where) -> int:
     """Elements between the token rows of t [>= rows][heads][dim], each row dense."""
-    n, h, d = t.shape if t.dim() == 3 else (-1, 0, 0)
-    s0, s1, s2 = t.stride() if n >= 0 else (0, 0, 0)
+    try:
+        n, h, d = t.shape
+    except ValueError:
+        raise RagError(2, where) from None
     if n < rows or h != heads or d != dim:
         raise RagError(2, where)
-    if t.dtype != dtype or t.get_device() != dev or s2 != 1 or (s1 != d and h != 1):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and h != 1) or t.dtype is not dtype or t.get_device() != dev:
         raise RagError(1, where)
     return s0 if n > 1 else max(s0, h * d)
 
@@ -395,20 +398,24 @@ def _append(fn, where, pool, dtype, layer, seqs, k, v, rope, q, q_out, device_er
     qs = hq = n_pos = 0
     qp = op = rp = None
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        qs = _row_stride(q, rows, hq, dim, dtype, dev, where)
-        if q_out is None or q_out.dtype != dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
+        if q_out is None:
             raise RagError(1, where)
-        if q_out.shape != q.shape:
+        shape = q.shape
+        hq = shape[1] if len(shape) == 3 else -1
+        qs = _row_stride(q, rows, hq, dim, dtype, dev, where)
+        if q_out.shape != shape:
             raise RagError(2, where)
+        if q_out.dtype is not dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
+            raise RagError(1, where)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise RagError(1, where)
     if rope is not None:
-        n_pos = rope.shape[0]
-        if rope.shape != (n_pos, dim // 2, 2):
+        shape = rope.shape
+        n_pos = shape[0]
+        if shape != (n_pos, dim // 2, 2):
             raise RagError(2, where)
-        if rope.dtype != torch.float32 or not rope.is_contiguous() or rope.get_device() != dev:
+        if rope.dtype is not torch.float32 or not rope.is_contiguous() or rope.get_device() != dev:
             raise RagError(1, where)
         rp = rope.data_ptr()
     if seqs.dev_index != dev:
