@@ -200,7 +200,9 @@ struct Kv8Params {
 //              be more than the CTAs, stretches are used after all.
 // One warp of a CTA walks the stretch and hands the items to the others
 // through a ring in shared memory.
-constexpr int kCost2 = 5, kCost1 = 3;      // weight of a key tile with two Q tiles and with one
+// weight of a key tile with two Q tiles and with one: 5 to 4 by measurement (16
+// prompts 140 us; 142 at 4 to 3, 149 at 5 to 3, 157 at 2 to 1)
+constexpr int kCost2 = 5, kCost1 = 4;
 constexpr int kMinWork = 2 * kCost2;       // least stretch of a CTA: two tiles
 constexpr int kMinWorkDecode = 2;
 constexpr int kReqCache = 16;              // requests whose geometry stays in shared memory
@@ -259,19 +261,22 @@ __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv
   const int B = p.batch.num_requests;
   const bool one_piece_each = p.part != nullptr;   // cut units: one piece a CTA
   bool pieces = p.split_tiles > 0;
-  for (int base = 0; base < min(B, kReqCache); base += 32)
-    if (base + lane < min(B, kReqCache)) ring->req[base + lane] = load_req(p.batch, base + lane);
-  __syncwarp();
+  // the first 32 requests stay in registers between the two rounds
+  ReqInfo mine = {};
+  if (lane < B) {
+    mine = load_req(p.batch, lane);
+    if (lane < kReqCache) ring->req[lane] = mine;
+  }
   int64_t carry = 0;   // 31 bits for every batch that agrees with its host totals
-  for (int round = 0; round < 2; ++round) {
+  for (;;) {
     carry = 0;
     for (int base = 0; base < B; base += 32) {
       const int b = base + lane;
       int64_t cnt = 0;
       if (b < B) {
-        const ReqInfo r = kv8_req(p, ring, b);
-        if (!req_ok(p.batch, r) && blockIdx.x == 0) atomicOr(p.err, kDevErrGeometry);
-        cnt = int64_t(p.num_kv_heads) * kv8_head_work(p, r, pieces);
+        if (base > 0) mine = load_req(p.batch, b);
+        if (!req_ok(p.batch, mine) && blockIdx.x == 0) atomicOr(p.err, kDevErrGeometry);
+        cnt = int64_t(p.num_kv_heads) * kv8_head_work(p, mine, pieces);
       }
       int64_t incl = cnt;
       for (int o = 1; o < 32; o <<= 1) {
@@ -283,6 +288,7 @@ __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv
     }
     if (!(pieces && one_piece_each && carry > p.grid)) break;
     pieces = false;
+    if (B > 32 && lane < B) mine = load_req(p.batch, lane);
   }
   __syncwarp();
   if (carry > INT32_MAX) {

@@ -85,9 +85,12 @@ struct Kv8Plan {
 };
 
 // Units of at most this many key tiles are not cut: one CTA walks them in less
-// time than the combine's launch and its reads of partial rows take.
-constexpr int kWholeTiles = 2, kWholeTilesDecode = 2;
+// time than the combine's launch and its reads of partial rows take (a step
+// over 5 tiles: 8.8 us cut in pieces of two, 9.7 us whole).
+constexpr int kWholeTiles = 2;
 // A piece's start and end (first loads, last products, its rows), in tiles.
+// (Counted as 8, the step of 16 requests is cut into pieces: 47 us against 38;
+// 2 gives the same plans as 4.)
 constexpr double kPieceTiles = 4.0;
 
 static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
@@ -99,7 +102,7 @@ static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms
   // capacities can give work to
   const int pages = kv8_tile_pages(pl.decode);
   const int tiles_max = std::max(1, cdiv(b.max_pages, pages));
-  pl.cut = tiles_max > (pl.decode ? kWholeTilesDecode : kWholeTiles) ? 1 : 0;
+  pl.cut = tiles_max > kWholeTiles ? 1 : 0;
   const double rt = cdiv(b.max_q, pl.toks_per_block);
   const double most = !pl.cut ? double(num_kv_heads) * (cdiv(b.total_q, pl.toks_per_block) + b.num_requests)
                               : num_kv_heads * rt * (double(b.num_page_refs) / pages + 2.0 * b.num_requests) *

@@ -27,11 +27,19 @@
 //   2 x 4 softmax warps: thread = row = TMEM lane; mask, online max and sum in
 //                   the log2 domain, P (fp16) to columns of its own
 // A tile is 80 keys: then S and P of both Q tiles have tensor-memory columns of
-// their own beside the two O (2 * 80 + 2 * 40 + 2 * 128 = 496 of 512), so that
-// S of the next tile is computed as soon as this one is in registers, under its
-// exponentials. With 128 keys P has to lie over S, and every tile pays the
-// round trip softmax -> PV -> QK -> softmax: 1.9-2.0 us for 128 keys against
-// %s here.
+// their own beside the two O (2 * 80 + 2 * 40 + 2 * 128 = 496 of 512), and S of
+// the next tile is computed as soon as this one is in registers, under its
+// exponentials. With 128 keys P has to lie over S and every tile pays the round
+// trip softmax -> PV -> QK -> softmax, but there are fewer of them. Measured
+// (128 / 80 keys): 506 / 530 us for 256 tokens of 64 heads over 65,792 keys,
+// 156 / 148 us for 16 prompts over ragged chunks, 41.3 / 41.8 us for 100 tokens
+// over 10,100 keys. 80 is kept: the ragged case is the usual one, and the
+// softmax warps spill nothing.
+// What bounds it: a tile of two Q tiles takes 2,700 cycles, of which the tensor
+// core is busy 1,450 (QK at N = 80 is bound by shared-memory reads of its
+// operands, 52 cycles a product against 40) and the exponential unit 1,280; with
+// exponentials, conversion and most products taken out of a copy it still takes
+// 1,900, so the rest is the chain of hand-offs between the roles.
 // Every wait is bounded; a timeout raises a device error instead of hanging.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -617,8 +625,8 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
           // Q tile 1 follows Q tile 0 by about half a tile: its PV waits for Q
           // tile 0's next S, so that one warpgroup's exponentials run while the
           // other one's S and O are made. (Issued tile by tile for both, the
-          // warpgroups run in step and share the exponential unit: 532 against
-          // %s us on the 70B-shaped prompt.)
+          // warpgroups run in step and share the exponential unit: 176 against
+          // 162 us on 16 prompts, in a version with both otherwise alike.)
           if (!qk(0, 0)) bad = 1;
           for (int i = 0; i <= n && !bad; ++i) {
             if (two && i < n && !qk(1, i)) { bad = 1; break; }
