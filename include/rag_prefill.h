@@ -41,8 +41,10 @@
  *     (the pool, the batch descriptors, q, kq, vq), none of which those
  *     kernels write, and writes global memory only after the previous kernel
  *     has completed. Kernels that write pool pages, page tables or the RoPE
- *     table (pool write, KV decode, recompute, RoPE table) and every kernel
- *     not of this library let the next kernel start only when they complete.
+ *     table (pool write, appends, KV decode, recompute, RoPE table) and every
+ *     kernel not of this library let the next kernel start only when they
+ *     complete. rag_kv8_attn's kernels release early too, and read q only
+ *     after the kernel before them has completed.
  */
 #ifndef RAG_PREFILL_H_
 #define RAG_PREFILL_H_
@@ -447,7 +449,8 @@ typedef struct {
  * (and at most 2^7 for V), with the largest new magnitude <= 448 * need; the
  * page's scale becomes need when the call writes its slot 0, else the larger
  * of need and the scale it has. New codes are e4m3(value / scale), rounded to
- * nearest even. Where the scale grows, the held codes become
+ * nearest even (for a caller's own scale that is no power of two: the value
+ * times the scale's rounded reciprocal). Where the scale grows, the held codes become
  * e4m3(code * old / new): exact but for values that fall below e4m3's normal
  * range, since the ratio is a power of two. Chunks are written by appending
  * their tokens to an empty sequence.

@@ -13,8 +13,16 @@
 namespace rag {
 
 constexpr int kMaxAppendSeqs = 65536;
-// Page blocks of K an SM from which an 8-bit append streams its rows.
+// An 8-bit append streams its rows through shared memory from this many page
+// blocks of K an SM on, where the deeper read-ahead pays for a block's longer
+// start, and from this many tokens a sequence on, as a sequence's unused units
+// leave the long blocks unequal. Streamed / not, at 8 heads unless said: 4
+// prompts of 256 tokens 9.5 / 7.4 us, of 512 (7 blocks an SM) 16.9 / 14.8, of
+// 1,024 (14) 24.7 / 28.7, of 2,048 41.7 / 51.4; 16 of 700, 2 heads (9) 27.8 /
+// 28.9; 2 of 2,048, 32 heads 38.9 / 53.0; 64 of 128 tokens 26.4 / 20.3, 32 of
+// 192 15.4 / 16.9, 64 of 256 33.7 / 36.0.
 constexpr int kStreamBlocksPerSm = 8;
+constexpr int kStreamTokensPerSeq = 144;
 
 static rag_status check_pool8(const rag_kv8_pool* pool) {
   if (!pool || !pool->k || !pool->v || !pool->k_scale || !pool->v_scale) return RAG_ERR_INVALID_ARG;
@@ -68,7 +76,10 @@ static rag_status check_append(AppendParams& p, int elem, int num_layers, int la
   p.n_pos = rope ? n_pos : 0;
   p.layer = layer;
   p.num_q_heads = q ? num_q_heads : 0;
-  // a power of two, as few as let every block (three an SM) start at once
+  // a power of two, as few as let every block (three an SM) start at once: its
+  // table rows and index arithmetic serve all of a block's tokens. At 8 / 4 / 2
+  // / 1 tokens a block, 16 prompts of up to 1,024 into 8 bits take 54 / 57 / 63
+  // / 81 us and 5 prompts of up to 700 fp32 tokens 5.3 / 7.1 / 8.5 / 11.9.
   p.tokens_per_block = 1;
   while (p.tokens_per_block < 8 && seqs->total_new > 3 * p.tokens_per_block * num_sms()) p.tokens_per_block *= 2;
   p.kv_blocks = 0;
@@ -218,7 +229,8 @@ rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_app
   const int64_t units = int64_t(seqs->total_new) / kPage + 2 * int64_t(seqs->n_seqs);   // see kv8_append_kernel
   const int q_blocks = q ? cdiv(seqs->total_new, p.tokens_per_block) : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (int64_t(seqs->total_new) / kPage * p.num_kv_heads >= kStreamBlocksPerSm * int64_t(num_sms())) {
+  if (int64_t(seqs->total_new) / kPage * p.num_kv_heads >= kStreamBlocksPerSm * int64_t(num_sms()) &&
+      seqs->total_new >= kStreamTokensPerSeq * int64_t(seqs->n_seqs)) {
     // many tokens: rows streamed through shared memory, queries in a launch of their own
     const int slots = 2 * num_sms();
     int64_t best = INT64_MAX;
@@ -229,9 +241,15 @@ rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_app
         p.units_per_block = n;
       }
     }
+    // fewer units than blocks the GPU holds: a unit's stages over several
+    // blocks (2 prompts of 512 tokens, 32 heads: 22.7 us -> 13.4). Never for
+    // its balance alone: two blocks a unit slow 32 chunks of 2,048 tokens from
+    // 99 to 145 us.
+    const int groups = cdiv(2 * p.num_kv_heads, 8);
+    p.heads_split = int(std::max<int64_t>(1, std::min<int64_t>(groups, slots / units)));
     {
       LaunchScope ls(kKindKv8Append, s);
-      cudaError_t e = launch_kv8_append_stream(p, cdiv(units, p.units_per_block), s);
+      cudaError_t e = launch_kv8_append_stream(p, cdiv(units, p.units_per_block) * p.heads_split, s);
       ls.done(e);
       if (e != cudaSuccess) return RAG_ERR_CUDA;
     }
@@ -243,10 +261,13 @@ rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_app
     }
     return RAG_OK;
   }
-  // a block takes several units once the GPU is filled a few times over, and
-  // with few units only 8 page blocks of one, so that no warp takes two
+  // a block takes several units once the GPU is filled a few times over (512
+  // sequences of 64 tokens, 8 heads: 71.7 us against 74.8 with one), and with
+  // fewer units than SMs only 8 page blocks of one, so that no warp takes two
+  // (64 tokens of 64 sequences 4.9 us against 5.8, 4 prompts of 256 7.5 against
+  // 8.3; but 64 prompts of 16 tokens, 192 units, 9.8 against 8.9)
   p.units_per_block = int(std::max<int64_t>(1, std::min<int64_t>(8, units / (8 * num_sms()))));
-  p.heads_split = units < 4 * num_sms() ? cdiv(2 * p.num_kv_heads, 8) : 1;
+  p.heads_split = units < num_sms() ? cdiv(2 * p.num_kv_heads, 8) : 1;
   const int64_t kv_blocks = (units + p.units_per_block - 1) / p.units_per_block * p.heads_split;
   if (kv_blocks + q_blocks >= (int64_t(1) << 31)) return RAG_ERR_UNSUPPORTED;
   p.kv_blocks = int(kv_blocks);

@@ -72,8 +72,9 @@ __device__ __forceinline__ Seq load_seq(const AppendSeqs& a, int s) {
   q.pos0 = a.pos0 ? __ldg(a.pos0 + s) : 0;
   q.n = t1 - q.t0;
   q.n_pages = p1 - q.p0;
-  q.ok = q.t0 >= 0 && q.n >= 0 && t1 <= a.total_new && q.start >= 0 && q.p0 >= 0 && q.n_pages >= 0 &&
-         p1 <= a.total_pages && int64_t(q.start) + q.n <= int64_t(q.n_pages) * kPage;
+  q.ok = q.t0 >= 0 && q.n >= 0 && t1 <= a.total_new &&
+         (q.n == 0 || (q.start >= 0 && q.p0 >= 0 && q.n_pages >= 0 && p1 <= a.total_pages &&
+                       int64_t(q.start) + q.n <= int64_t(q.n_pages) * kPage));
   return q;
 }
 
@@ -769,20 +770,21 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
     fence_mbar_init();
   }
   if (warp < p.units_per_block) {
-    const Unit u = unit_of(p, int(blockIdx.x) * p.units_per_block + warp, lane);
+    const Unit u = unit_of(p, int(blockIdx.x) / p.heads_split * p.units_per_block + warp, lane);
     if (lane == 0) ctl->units[warp] = u;
   }
   __syncthreads();
   volatile int* abort_flag = &ctl->abort;
   const int H = p.num_kv_heads;
-  const int groups = (2 * H + 7) / 8;   // stages of a unit
+  const int groups = (2 * H + 7) / 8;   // stages of a unit, shared by heads_split blocks
+  const int y0 = int(blockIdx.x) % p.heads_split;
   if (warp == 16) {
     uint32_t n = 0;
     bool bad = false;
     for (int i = 0; i < p.units_per_block && !bad; ++i) {
       const Unit u = ctl->units[i];
       if (u.page < 0) continue;
-      for (int y = 0; y < groups; ++y, ++n) {
+      for (int y = y0; y < groups; y += p.heads_split, ++n) {
         const int s = n % kStreamStages;
         if (n >= uint32_t(kStreamStages) && !mbar_wait(&ctl->empty[s], (n / kStreamStages - 1) & 1, abort_flag)) {
           bad = true;
@@ -833,7 +835,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
   for (int i = 0; i < p.units_per_block; ++i) {
     const Unit u = ctl->units[i];
     if (u.page < 0) continue;
-    for (int y = 0; y < groups; ++y, ++n) {
+    for (int y = y0; y < groups; y += p.heads_split, ++n) {
       const int s = n % kStreamStages;
       if (!mbar_wait(&ctl->full[s], (n / kStreamStages) & 1, abort_flag)) {
         if (lane == 0 && p.err) atomicOr(p.err, kDevErrTimeout);

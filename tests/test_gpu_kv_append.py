@@ -392,7 +392,8 @@ def test_offsets_past_32_bits():
 # calls with many tokens stream their rows through shared memory
 @pytest.mark.parametrize("fused,pad,rope", [(False, 0, True), (True, 5, True), (False, 0, False)])
 @pytest.mark.parametrize("H,starts,news", [(32, [0, 5, 31, 16], [300, 1, 170, 160]), (3, [7, 0], [3000, 3400]),
-                                           (1, [0], [19000]), (20, [3, 15, 0], [500, 17, 513])])
+                                           (1, [0], [19000]), (20, [3, 15, 0], [500, 17, 513]),
+                                           (8, [3, 0], [1500, 1300])])
 def test_streamed_calls(H, starts, news, fused, pad, rope):
     case = Case("e4m3", starts, news, H=H, G=2, fused=fused, pad=pad, seed=H, n_pos=20000, rope=rope)
     before = case.state()
@@ -419,6 +420,25 @@ def test_streamed_calls_give_the_bits_of_small_ones():
     for x, y in zip(a.state(), b.state()):
         np.testing.assert_array_equal(x, y)
     assert torch.equal(a.q_out, b.q_out)
+
+
+# a sequence that appends nothing is not looked at: its start and pages may be anything
+@pytest.mark.parametrize("kind", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("n", [3, 3000])
+def test_a_sequence_of_no_tokens_is_skipped(kind, n):
+    case = Case(kind, [5, 0, 2], [n, 0, n], H=8, seed=n, n_pos=8192)
+    tok, start, po, ids, pos0 = case.arrays
+    before = case.state()
+    case.run()
+    want = case.state()
+    other = Case(kind, [5, 0, 2], [n, 0, n], H=8, seed=n, n_pos=8192)
+    bad = list(start)
+    bad[1] = 1 << 20
+    other.append_c = sp.Append(tok, bad, po, ids, pos0=pos0)
+    other.run()
+    for x, y in zip(other.state(), want):
+        np.testing.assert_array_equal(x, y)
+    assert torch.equal(other.q_out, case.q_out) and int(other.err.item()) == int(case.err.item()) == 0
 
 
 def test_streamed_infinities_bad_pages_and_positions():
