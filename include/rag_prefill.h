@@ -412,7 +412,8 @@ RAG_API rag_status rag_rope_cos_sin(double base, int32_t head_dim, int32_t n_pos
  *       V is stored like rag_kv_pool_write's (a bf16 pool keeps fp16)
  * q     optional: [total_new] rows of num_q_heads * head_dim values, q_stride
  *       elements apart, rotated the same way into the dense
- *       q_out [total_new][num_q_heads][head_dim] (may be q itself when dense)
+ *       q_out [total_new][num_q_heads][head_dim] (may be q itself when dense;
+ *       otherwise it must not overlap q, k or v)
  * When the call writes slot 0 of a page, the page's slots behind the call's
  * last token are zeroed; other slots keep what they hold.
  * *device_err (optional device int32) collects bits: 1 a page id outside the
@@ -478,7 +479,7 @@ RAG_API size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch*
  * captured call, within the host totals and maxima of `batch`, which then are
  * capacities.
  * q       [total_q][num_q_heads][128] bf16, device
- * o       [total_q][num_q_heads][128] bf16
+ * o       [total_q][num_q_heads][128] bf16, not overlapping q
  * row_lse optional [total_q][num_q_heads] fp32
  * num_q_heads / num_kv_heads may be any whole number up to 128. sm_scale <= 0
  * selects 1 / sqrt(128).

@@ -34,6 +34,11 @@ bool make_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, 
 int num_sms();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether two ranges of bytes share one.
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + uintptr_t(b_bytes) && y < x + uintptr_t(a_bytes);
+}
 inline int cdiv(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 rag_status check_pool(const rag_kv_pool* pool);

@@ -56,6 +56,12 @@ static rag_status check_append(AppendParams& p, int elem, int num_layers, int la
   if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(rope) ||
       (k_stride * elem) % 16 || (v_stride * elem) % 16 || (q && (q_stride * elem) % 16))
     return RAG_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(device_err) & 3u) return RAG_ERR_INVALID_ARG;
+  const int64_t n = seqs->total_new, out_bytes = n * q_row * elem;
+  const auto span = [&](int64_t stride, int64_t row) { return ((n - 1) * stride + row) * elem; };
+  if ((q != q_out && overlap(q_out, out_bytes, q, span(q_stride, q_row))) ||
+      overlap(q_out, out_bytes, k, span(k_stride, kv_row)) || overlap(q_out, out_bytes, v, span(v_stride, kv_row)))
+    return RAG_ERR_INVALID_ARG;
   p.seqs.tok_off = seqs->tok_off;
   p.seqs.start = seqs->start;
   p.seqs.page_off = seqs->page_off;
@@ -292,6 +298,8 @@ rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch
   if (b.total_q > 0 && (!q || !o)) return RAG_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || (reinterpret_cast<uintptr_t>(row_lse) & 3u)) return RAG_ERR_INVALID_ARG;
   if (!std::isfinite(sm_scale)) return RAG_ERR_INVALID_ARG;
+  const int64_t q_bytes = int64_t(b.total_q) * num_q_heads * kHeadDim * 2;
+  if (overlap(q, q_bytes, o, q_bytes)) return RAG_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return RAG_ERR_WORKSPACE;
   const int H = pool->num_kv_heads, G = num_q_heads / H;
   const Kv8Plan pl = plan_kv8(b, H, G, num_sms());

@@ -714,69 +714,83 @@ __global__ void __launch_bounds__(256) kv8_split_q_kernel(const Kv8Params p, int
 
 // Merge the partial rows (O, m, l) of every cut unit:
 //   m = max_s m_s, l = sum_s l_s 2^(m_s - m), O = sum_s O_s l_s 2^(m_s - m) / l.
-// Block (c, y) merges 8 kRowsWarp rows of the unit whose second piece CTA c left
-// (nothing for other CTAs); a warp takes a row at a time, each lane 4 of the 128
-// columns; lane j holds the statistics of piece s0 + j, and the O slices of
-// kBatch pieces are requested before any is used. Stretches leave two or three
-// pieces a unit (4 at a time, two rows a warp, all 64 warps of an SM), pieces
-// up to a dozen (16 at a time, a row a warp). (A warp per output row of the
-// batch, each finding its own pieces, took 45 us on 16 requests of 32-128
-// tokens.)
-template <int kBatch, int kRowsWarp, int kBlocks>
+// Block (c, y) merges 16 kPairs rows of the unit whose second piece CTA c left
+// (nothing for other CTAs); a warp takes two rows at a time, 16 lanes each, a
+// lane 8 of the 128 columns; lane j of a row holds the statistics of piece
+// s0 + j, and the O slices of kBatch pieces are requested before any is used.
+// Stretches leave two or three pieces a unit (4 at a time), pieces up to a
+// dozen (8 at a time). Bound by its instructions per row: with a row to a warp
+// 16 requests of 32-128 tokens took 139.9 us in all, so 136.3; a decode step is
+// the same either way.
+template <int kBatch, int kPairs, int kBlocks>
 __global__ void __launch_bounds__(256, kBlocks) kv8_combine_kernel(const Kv8Params p) {
-  constexpr int kRows = 8 * kRowsWarp;
+  constexpr int kRows = 16 * kPairs;
   pdl_launch_dependents();
   pdl_wait();   // partials and cuts come from the attention kernel
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_in = threadIdx.x >> 4, lane = threadIdx.x & 15;
   const int4 c4 = __ldcg(reinterpret_cast<const int4*>(p.cuts + blockIdx.x));
   const int c1 = __ldcg(&p.cuts[blockIdx.x].c1);
   const int n_tok = c4.x, tok0 = c4.y, head0 = c4.z, c0 = c4.w;
   if (n_tok == 0) return;
   const int G = p.group;
+  const int inv_g = (65536 + G - 1) / G;   // r / G = r inv_g >> 16 for r < 128
   const int TT = p.decode ? p.toks_per_block : p.toks_per_block / kQTiles;   // tokens of a Q tile
   const int n_piece = c1 - c0 + 1;
-  const size_t slot = size_t(p.item_rows) * kPartStride;
-  for (int rr = blockIdx.y * kRows + warp; rr < min(p.item_rows, int(blockIdx.y + 1) * kRows); rr += 8) {
-    const int r = rr % kBM, tok = rr / kBM * TT + r / G;
-    if (r >= TT * G || tok >= n_tok) continue;   // uniform over the warp
-    const float* row0 = p.part + size_t(2 * c0) * slot + size_t(rr) * kPartStride;
-    auto piece = [&](int i) { return row0 + (i == 0 ? slot : size_t(2 * i) * slot); };
+  const uint32_t slot = uint32_t(p.item_rows) * kPartStride;
+  for (int k = 0; k < kPairs; ++k) {
+    const int rr = int(blockIdx.y) * kRows + 16 * k + row_in;
+    const int r = rr % kBM, tok_t = (r * inv_g) >> 16, tok = rr / kBM * TT + tok_t;
+    const bool live = r < TT * G && tok < n_tok;
+    if (!__any_sync(0xffffffffu, live)) continue;
+    const float* first = p.part + (size_t(2 * c0) + 1) * slot + uint32_t(rr) * kPartStride;
+    const float* rest = first - slot;   // piece i > 0 lies 2 i slots on
+    auto piece = [&](int i) { return i == 0 ? first : rest + size_t(2 * i) * slot; };
     constexpr int kStatOff = kHeadDim / 2;   // 32-bit word of m (then l) in a row
     float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float acc[8] = {};
     for (int s0 = 0; s0 < n_piece; s0 += kBatch) {
-      const float2 ml = (lane < kBatch && s0 + lane < n_piece)
+      const float2 ml = (live && lane < kBatch && s0 + lane < n_piece)
                             ? __ldcg(reinterpret_cast<const float2*>(piece(s0 + lane) + kStatOff))
                             : make_float2(-INFINITY, 0.f);
-      uint2 v[kBatch];
+      uint4 v[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        v[j] = s0 + j < n_piece ? __ldcg(reinterpret_cast<const uint2*>(piece(s0 + j)) + lane) : make_uint2(0u, 0u);
+        v[j] = live && s0 + j < n_piece ? __ldcg(reinterpret_cast<const uint4*>(piece(s0 + j)) + lane)
+                                        : make_uint4(0u, 0u, 0u, 0u);
       float mb = fmaxf(m, ml.x);
-      for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+      for (int o = 8; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
       const float mu = (mb == -INFINITY) ? 0.f : mb;
       if (s0 > 0) {
         const float sc = (m == -INFINITY) ? 0.f : ex2(m - mu);
         l *= sc;
-        acc.x *= sc; acc.y *= sc; acc.z *= sc; acc.w *= sc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] *= sc;
       }
       m = mb;
       const float wl = (ml.x == -INFINITY) ? ml.y : ml.y * ex2(ml.x - mu);   // l = 0 there, or nan
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        const float wgt = __shfl_sync(0xffffffffu, wl, j);
-        const float2 lo = f16x2_to_f32x2(v[j].x), hi = f16x2_to_f32x2(v[j].y);
+        const float wgt = __shfl_sync(0xffffffffu, wl, j, 16);
+        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
         l += wgt;
-        acc.x += lo.x * wgt; acc.y += lo.y * wgt; acc.z += hi.x * wgt; acc.w += hi.y * wgt;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = f16x2_to_f32x2(w[i]);
+          acc[2 * i] += x.x * wgt;
+          acc[2 * i + 1] += x.y * wgt;
+        }
       }
     }
+    if (!live) continue;
     const float m_use = (m == -INFINITY) ? 0.f : m;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t orow = int64_t(tok0 + tok) * p.num_q_heads + head0 + r % G;
-    uint2 out;
-    out.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    out.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2*>(p.o + orow * kHeadDim)[lane] = out;
+    const int64_t orow = int64_t(tok0 + tok) * p.num_q_heads + head0 + (r - tok_t * G);
+    uint4 out;
+    out.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    out.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+    out.z = pack_bf16x2(acc[4] * inv, acc[5] * inv);
+    out.w = pack_bf16x2(acc[6] * inv, acc[7] * inv);
+    reinterpret_cast<uint4*>(p.o + orow * kHeadDim)[lane] = out;
     if (lane == 0 && p.row_lse) p.row_lse[orow] = (m_use + __log2f(l)) * 0.69314718055994531f;
   }
 }
@@ -799,8 +813,8 @@ cudaError_t launch_kv8_fwd(const CUtensorMap& tq, const CUtensorMap& tk, const C
 
 cudaError_t launch_kv8_combine(const Kv8Params& p, cudaStream_t stream) {
   if (p.split_tiles > 0)
-    return launch_pdl(kv8_combine_kernel<16, 1, 4>, dim3(p.grid, p.item_rows / 8), dim3(256), 0, stream, 1, p);
-  return launch_pdl(kv8_combine_kernel<4, 2, 8>, dim3(p.grid, p.item_rows / 16), dim3(256), 0, stream, 1, p);
+    return launch_pdl(kv8_combine_kernel<8, 1, 4>, dim3(p.grid, p.item_rows / 16), dim3(256), 0, stream, 1, p);
+  return launch_pdl(kv8_combine_kernel<4, 2, 6>, dim3(p.grid, (p.item_rows + 16) / 32), dim3(256), 0, stream, 1, p);
 }
 
 }  // namespace rag

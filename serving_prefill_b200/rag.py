@@ -413,12 +413,15 @@ def _append(fn, where, pool, dtype, layer, seqs, k, v, rope, q, q_out, device_er
     if rope is not None:
         shape = rope.shape
         n_pos = shape[0]
-        if shape != (n_pos, dim // 2, 2):
+        if shape != (n_pos, dim // 2, 2) or n_pos == 0:
             raise RagError(2, where)
         if rope.dtype is not torch.float32 or not rope.is_contiguous() or rope.get_device() != dev:
             raise RagError(1, where)
         rp = rope.data_ptr()
     if seqs.dev_index != dev:
+        raise RagError(1, where)
+    if device_err is not None and (device_err.dtype is not torch.int32 or device_err.numel() == 0
+                                   or device_err.get_device() != dev):
         raise RagError(1, where)
     status = fn(pool.ref, layer, seqs.ref, k.data_ptr(), ks, v.data_ptr(), vs, rp, n_pos, qp, qs, hq, op,
                 None if device_err is None else device_err.data_ptr(), _on(dev, stream))

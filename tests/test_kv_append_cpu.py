@@ -25,17 +25,17 @@ def seqs(n=2, total=10, pages=4, tok=0x1000, start=0x2000, po=0x3000, pid=0x4000
 
 
 def call(pool, s, fn=None, layer=0, k=0x50000, ks=1024, v=0x60000, vs=1024, rope=0x70000, n_pos=100, q=0x80000,
-         qs=4096, hq=32, q_out=0x90000):
+         qs=4096, hq=32, q_out=0x200000, err=None):
     fn = fn or (lib().rag_kv8_append if isinstance(pool, RagKV8Pool) else lib().rag_kv_append)
     return fn(ctypes.byref(pool) if pool is not None else None, layer, ctypes.byref(s) if s is not None else None, k, ks,
-              v, vs, rope, n_pos, q, qs, hq, q_out, None, None)
+              v, vs, rope, n_pos, q, qs, hq, q_out, err, None)
 
 
 @pytest.mark.parametrize("pool", [pool16(), pool8()], ids=["bf16", "e4m3"])
 def test_arguments_are_refused_before_a_launch(pool):
     assert call(pool, None) == INVALID
     for bad in (dict(layer=2), dict(layer=-1), dict(k=None), dict(v=None), dict(k=0x50008), dict(v=0x60004),
-                dict(rope=0x70008), dict(q=0x80004), dict(q_out=0x90008), dict(q_out=None), dict(q=None),
+                dict(rope=0x70008), dict(q=0x80004), dict(q_out=0x200008), dict(q_out=None), dict(q=None),
                 dict(n_pos=0), dict(ks=1028), dict(vs=1025), dict(qs=4100), dict(q=0x80000, q_out=0x80000, qs=6144)):
         assert call(pool, seqs(), **bad) == INVALID, bad
     for bad in (dict(ks=1016), dict(vs=0), dict(qs=4088), dict(hq=0)):
@@ -64,6 +64,29 @@ def test_pools_are_checked():
     assert call(pool8(layers=0), seqs()) == SHAPE
     assert call(pool8(layers=1 << 12, pages=1 << 12), seqs()) == UNSUPPORTED   # 2^27 page blocks
     assert call(pool16(head_dim=64), seqs()) == UNSUPPORTED                    # bf16 needs head_dim 128
+
+
+def test_outputs_that_overlap_inputs_are_refused():
+    """10 tokens: rows of 8 KB of queries, 2 KB of k at 0x50000 and of v at 0x60000."""
+    for out in (0x80000 + 16, 0x80000 - 16, 0x80000 + 10 * 8192 - 16,
+                0x50000, 0x50000 + 9 * 2048, 0x60000 - 10 * 8192 + 16):
+        assert call(pool8(), seqs(), q_out=out) == INVALID, hex(out)
+    assert call(pool8(), seqs(), err=0x400002) == INVALID
+    assert attend(pool8(), batch(), q=0x400000, o=0x400000) == INVALID
+    assert attend(pool8(), batch(), q=0x400000, o=0x400000 + 30 * 32 * 256 - 16) == INVALID
+
+
+def test_binding_checks_the_error_word_and_the_table():
+    pool = sp.KV8Pool(1, 4, 2, device="cpu")
+    s = sp.Append([0, 3], [0], [0, 1], [2], device="cpu")
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    for err in (torch.zeros(1), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(sp.RagError) as e:
+            sp.rag_kv8_append(pool, 0, s, k, k, device_err=err)
+        assert e.value.status == INVALID
+    with pytest.raises(sp.RagError) as e:
+        sp.rag_kv8_append(pool, 0, s, k, k, rope=torch.zeros(0, 64, 2))   # no table is rope=None
+    assert e.value.status == SHAPE
 
 
 def test_table_of_rotations_is_checked():
@@ -118,7 +141,7 @@ def batch(B=2, q=(10, 20), docs=(100, 50)):
                     0x30000, 0x31000, 0x32000, 0x33000, 0x34000)
 
 
-def attend(pool, b, hq=32, layer=0, q=0x40000, o=0x70000, lse=None, ws=0x80000, ws_bytes=1 << 40, scale=0.0, causal=1):
+def attend(pool, b, hq=32, layer=0, q=0x40000, o=0x100000, lse=None, ws=0x80000, ws_bytes=1 << 40, scale=0.0, causal=1):
     return lib().rag_kv8_attn(ctypes.byref(pool), layer, ctypes.byref(b) if b is not None else None, q, hq, scale,
                               causal, o, lse, ws, ws_bytes, None)
 
