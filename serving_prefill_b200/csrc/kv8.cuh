@@ -223,32 +223,48 @@ struct Kv8Ring {
   ReqInfo req[kReqCache];
 };
 
+// The walk's code runs cold in every launch, before the first load of a page,
+// so it is kept short: the kernel for at most 16 rows has one block a request
+// by construction, and no loop is unrolled. (With the block count and tile size
+// of both kernels in one code a decode step's first item came 2.8 us after the
+// line was known.)
+template <bool kDecode>
 __device__ __forceinline__ int kv8_blocks(const Kv8Params& p, const ReqInfo& r) {
-  return r.n_q <= 0 || !req_ok(p.batch, r) ? 0 : ceil_div(r.n_q, p.toks_per_block);
+  if (r.n_q <= 0 || !req_ok(p.batch, r)) return 0;
+  return kDecode ? 1 : ceil_div(r.n_q, p.toks_per_block);
 }
+__host__ __device__ constexpr int kv8_tile_pages(int decode) { return decode ? kPagesPerTile : kFwdPages; }
 // Key tiles of block rb, at least one (a request without pages writes its zeros
 // from a fully masked tile). Causal: the pages behind the block's last visible
 // key are left out; a page holds at most 16 of the tokens that lie behind it,
 // so floor(tokens / 16) whole pages do.
-__host__ __device__ constexpr int kv8_tile_pages(int decode) { return decode ? kPagesPerTile : kFwdPages; }
+template <bool kDecode>
 __device__ __forceinline__ int kv8_tiles(const Kv8Params& p, const ReqInfo& r, int rb) {
   int pages = r.n_pages;
-  if (p.causal) pages -= min(max(r.n_q - (rb + 1) * p.toks_per_block, 0), r.n_doc) / kPage;
-  return max(1, ceil_div(pages, kv8_tile_pages(p.decode)));
+  if (p.causal) {
+    const int behind = kDecode ? 0 : max(r.n_q - (rb + 1) * p.toks_per_block, 0);
+    pages -= min(behind, r.n_doc) / kPage;
+  }
+  return max(1, ceil_div(pages, kv8_tile_pages(kDecode)));
 }
+template <bool kDecode>
 __device__ __forceinline__ int kv8_cost(const Kv8Params& p, const ReqInfo& r, int rb) {
-  if (p.decode) return 1;
+  if (kDecode) return 1;
   return r.n_q - rb * p.toks_per_block > p.toks_per_block / kQTiles ? kCost2 : kCost1;
 }
+template <bool kDecode>
 __device__ __forceinline__ int kv8_weight(const Kv8Params& p, const ReqInfo& r, int rb, bool pieces) {
-  const int n = kv8_tiles(p, r, rb);
-  return pieces ? ceil_div(n, p.split_tiles) : n * kv8_cost(p, r, rb);
+  const int n = kv8_tiles<kDecode>(p, r, rb);
+  return pieces ? ceil_div(n, p.split_tiles) : n * kv8_cost<kDecode>(p, r, rb);
 }
 // Weight of one KV head of a request.
+template <bool kDecode>
 __device__ __forceinline__ int kv8_head_work(const Kv8Params& p, const ReqInfo& r, bool pieces) {
-  const int n = kv8_blocks(p, r);
+  const int n = kv8_blocks<kDecode>(p, r);
+  if (kDecode) return n ? kv8_weight<kDecode>(p, r, 0, pieces) : 0;
   int w = 0;
-  for (int rb = 0; rb < n; ++rb) w += kv8_weight(p, r, rb, pieces);
+#pragma unroll 1
+  for (int rb = 0; rb < n; ++rb) w += kv8_weight<kDecode>(p, r, rb, pieces);
   return w;
 }
 __device__ __forceinline__ ReqInfo kv8_req(const Kv8Params& p, const Kv8Ring* ring, int b) {
@@ -257,6 +273,7 @@ __device__ __forceinline__ ReqInfo kv8_req(const Kv8Params& p, const Kv8Ring* ri
 
 // The line of the batch (one warp): each request's weight as an exclusive
 // prefix, the total, a CTA's stretch.
+template <bool kDecode>
 __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv8Ring* ring, int lane) {
   const int B = p.batch.num_requests;
   const bool one_piece_each = p.part != nullptr;   // cut units: one piece a CTA
@@ -270,13 +287,14 @@ __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv
   int64_t carry = 0;   // 31 bits for every batch that agrees with its host totals
   for (;;) {
     carry = 0;
+#pragma unroll 1
     for (int base = 0; base < B; base += 32) {
       const int b = base + lane;
       int64_t cnt = 0;
       if (b < B) {
         if (base > 0) mine = load_req(p.batch, b);
         if (!req_ok(p.batch, mine) && blockIdx.x == 0) atomicOr(p.err, kDevErrGeometry);
-        cnt = int64_t(p.num_kv_heads) * kv8_head_work(p, mine, pieces);
+        cnt = int64_t(p.num_kv_heads) * kv8_head_work<kDecode>(p, mine, pieces);
       }
       int64_t incl = cnt;
       for (int o = 1; o < 32; o <<= 1) {
@@ -300,13 +318,14 @@ __device__ __forceinline__ void kv8_line(const Kv8Params& p, int32_t* prefix, Kv
     const int W = int(carry);
     prefix[B] = W;
     ring->total = W;
-    ring->stretch = max(int((uint32_t(W) + p.grid - 1) / p.grid), pieces ? 1 : p.decode ? kMinWorkDecode : kMinWork);
+    ring->stretch = max(int((uint32_t(W) + p.grid - 1) / p.grid), pieces ? 1 : kDecode ? kMinWorkDecode : kMinWork);
     ring->pieces = pieces ? 1 : 0;
   }
   __syncwarp();
 }
 
 // The items of one CTA in order (warp-uniform).
+template <bool kDecode>
 struct Kv8Walk {
   int pos, end, b, per_head;
   ReqInfo req;
@@ -327,24 +346,29 @@ struct Kv8Walk {
     while (pos < end) {
       if (b < 0 || prefix[b + 1] <= pos) {
         int lo = b < 0 ? 0 : b + 1, hi = p.batch.num_requests - 1;
+#pragma unroll 1
         while (lo < hi) {  // last request with prefix <= pos
           const int mid = (lo + hi + 1) >> 1;
           if (prefix[mid] <= pos) lo = mid; else hi = mid - 1;
         }
         b = lo;
         req = kv8_req(p, ring, b);
-        per_head = kv8_head_work(p, req, pieces);
+        per_head = kv8_head_work<kDecode>(p, req, pieces);
       }
       int rem = pos - prefix[b];
       it.g = rem / per_head;
       rem -= it.g * per_head;
       it.rb = 0;
-      int w = kv8_weight(p, req, 0, pieces);
-      while (rem >= w) {
-        rem -= w;
-        w = kv8_weight(p, req, ++it.rb, pieces);
+      int w = per_head;
+      if (!kDecode) {
+        w = kv8_weight<kDecode>(p, req, 0, pieces);
+#pragma unroll 1
+        while (rem >= w) {
+          rem -= w;
+          w = kv8_weight<kDecode>(p, req, ++it.rb, pieces);
+        }
       }
-      const int s = pos - rem, n = kv8_tiles(p, req, it.rb), cost = kv8_cost(p, req, it.rb);
+      const int s = pos - rem, n = kv8_tiles<kDecode>(p, req, it.rb), cost = kv8_cost<kDecode>(p, req, it.rb);
       int t_begin, t_end;
       if (pieces) {
         const int q = n / w, r = n % w;           // piece i: q tiles, the first r pieces one more

@@ -360,9 +360,9 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // ------------------------------------------------------------ producer
     uint32_t t_glob = 0, n_k = 0, n_v = 0;   // n_k, n_v: K and V tiles issued
     int bad = 0;
-    Kv8Walk walk;
+    Kv8Walk<true> walk;
     int cached_b = -1;
-    kv8_line(p, prefix, &ctl->ring, lane);
+    kv8_line<true>(p, prefix, &ctl->ring, lane);
     walk.start(&ctl->ring);
     while (!bad && walk.next(p, prefix, &ctl->ring, it)) {
       if (!kv8_put(&ctl->ring, n_it++, it, lane, abort_flag)) { bad = 1; break; }

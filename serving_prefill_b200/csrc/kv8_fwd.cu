@@ -409,9 +409,9 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       // ------------------------------------------------------------ producer
       uint32_t t_glob = 0, n_k = 0, n_v = 0;   // n_k, n_v: K and V tiles issued
       int bad = 0;
-      Kv8Walk walk;
+      Kv8Walk<false> walk;
       int cached_b = -1;
-      kv8_line(p, prefix, &ctl->ring, lane);
+      kv8_line<false>(p, prefix, &ctl->ring, lane);
       walk.start(&ctl->ring);
       while (!bad && walk.next(p, prefix, &ctl->ring, it)) {
         if (!kv8_put(&ctl->ring, n_it++, it, lane, abort_flag)) { bad = 1; break; }
