@@ -375,7 +375,8 @@ RAG_API rag_status rag_recompute_status(const void* plan, int32_t* counts, void*
  * pointers. Sequence s takes rows tok_off[s] .. tok_off[s+1]-1 of k, v and q as
  * its tokens start[s], start[s]+1, ...; its token i lives in slot i % 16 of page
  * page_ids[page_off[s] + i / 16] and has rotary position pos0[s] + i.
- *   tok_off  [n_seqs+1]   prefix over sequences of new tokens (0 is allowed)
+ *   tok_off  [n_seqs+1]   prefix over sequences of new tokens, from 0 (a sequence
+ *                         may have none: it is not looked at)
  *   start    [n_seqs]     tokens the sequence holds already
  *   page_off [n_seqs+1]   prefix over sequences of pages; they must hold
  *                         start[s] + new tokens
@@ -488,8 +489,9 @@ RAG_API size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch*
  * to 2^-14 of the row's largest, 2^-18 of it absolute), K as its codes, with
  * fp32 sums; the softmax runs in fp32; the weights enter the second product in
  * at least 11 bits (those below 2^-14 of the row's largest with an error of at
- * most 2^-24 of it), V exactly, with fp32 sums. A nan or an infinity in a query
- * makes that row nan.
+ * most 2^-24 of it), V exactly, with fp32 sums (for a caller's own scale that is
+ * no power of two, or below 2^-24, query blocks of more than 16 rows take code *
+ * scale rounded to fp16). A nan or an infinity in a query makes that row nan.
  * The workspace's error word collects page, geometry and timeout errors as
  * rag_fused_prefill_attn's, and RAG_ERR_RANGE for a scale outside the range
  * above (it is taken as 1). */

@@ -352,7 +352,12 @@ __device__ __forceinline__ Unit unit_of(const AppendParams& p, int u, int lane) 
     if (report) atomicOr(p.err, kDevErrGeometry);
     return x;
   }
-  const int a = q.start / kPage + (u - (q.t0 / kPage + 2 * s));     // page of the sequence
+  const int first = q.t0 / kPage + 2 * s;   // above u only if tok_off does not rise from 0
+  if (u < first) {
+    if (report) atomicOr(p.err, kDevErrGeometry);
+    return x;
+  }
+  const int a = q.start / kPage + (u - first);     // page of the sequence
   if (q.n == 0 || a < 0 || a > (q.start + q.n - 1) / kPage) return x;
   const int page = __ldg(p.seqs.page_ids + q.p0 + a);
   if (page < 0 || page >= p.num_pages) {

@@ -327,6 +327,28 @@ def test_inconsistent_descriptors_are_reported_and_write_nothing(kind, what):
         np.testing.assert_array_equal(after[1][pg], before[1][pg])
 
 
+@pytest.mark.parametrize("kind,H,n", [("bf16", 2, 20), ("e4m3", 2, 20), ("e4m3", 32, 700)])
+def test_rows_before_the_first_sequence_are_reported(kind, H, n):
+    """tok_off that does not begin at 0: its rows belong to the sequence all the
+    same, the 16 before them to none (their q_out rows become zeros)."""
+    case = Case(kind, [40], [n], H=H, G=1, seed=16)
+    tok, start, po, ids, pos0 = case.arrays
+    before = case.state()
+    case.run()
+    want, q_want = case.state(), case.q_out.clone()
+    other = Case(kind, [40], [n], H=H, G=1, seed=16)
+    pad = lambda x: torch.cat([torch.full_like(x[:16], 3.0), x])  # noqa: E731
+    other.k, other.v, other.q = pad(other.k), pad(other.v), pad(other.q)
+    other.q_out = torch.full_like(other.q, 7.0)
+    other.append_c = sp.Append([16, 16 + n], start, po, ids, pos0=pos0)
+    other.run()
+    for x, y in zip(other.state(), want):
+        np.testing.assert_array_equal(x, y)
+    assert torch.equal(other.q_out[16:], q_want) and not other.q_out[:16].any()
+    assert int(other.err.item()) == 2 and int(case.err.item()) == 0
+    np.testing.assert_array_equal(before[0][ids[0]], want[0][ids[0]])
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_captured_steps_advance_on_the_device(kind):
     """One captured append of one token per sequence, replayed 20 times while
