@@ -201,7 +201,7 @@ struct Kv8Params {
 // One warp of a CTA walks the stretch and hands the items to the others
 // through a ring in shared memory.
 // weight of a key tile with two Q tiles and with one: 5 to 4 by measurement (16
-// prompts 140 us; 142 at 4 to 3, 149 at 5 to 3, 157 at 2 to 1)
+// prompts 140 us when it was set; 142 at 4 to 3, 149 at 5 to 3, 157 at 2 to 1)
 constexpr int kCost2 = 5, kCost1 = 4;
 constexpr int kMinWork = 2 * kCost2;       // least stretch of a CTA: two tiles
 constexpr int kMinWorkDecode = 2;
