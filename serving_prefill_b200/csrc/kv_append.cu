@@ -573,10 +573,15 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv8_append_kernel(const App
   __syncthreads();
   int err = 0;
   const int H = p.num_kv_heads;
+  // The table buffers alternate with the units that have work: between two fills
+  // of one buffer lies the barrier of the unit between them, which every warp
+  // reaches only when it has read the first. (By the unit's number they would
+  // not: a unit without a page has no barrier.)
+  float4* rows = tab;
   for (int i = 0; i < p.units_per_block; ++i) {
     const Unit u = units[i];
     if (u.page < 0) continue;
-    float4* rows = tab + (i & 1) * (kPage * 32);   // the buffer before the last sync's is free
+    rows = rows == tab ? tab + kPage * 32 : tab;
     if (p.rope) {
       for (int f = u.s0 * 32 + tid; f < u.s1 * 32; f += kAppendThreads) {
         const int pos = u.pos + (f >> 5);
