@@ -511,7 +511,10 @@ RAG_API rag_status rag_last_device_error(void* workspace, int32_t* bits, void* s
  * (1 .. 2e9 ns), while a second role waits on another such barrier with the
  * pipelines' full 2 s limit. The first wait runs out, records the timeout bit
  * (4) in *device_err (device int32, OR-ed in) and raises the CTA's abort flag;
- * the second role must then leave at once. The kernel therefore ends after
+ * the second role must then leave at once. Beside them four warps go through
+ * rounds of a named barrier they share; one gives up such a wait before the
+ * third round, and all four must leave at that round (else bit 2 is recorded).
+ * The kernel therefore ends after
  * about limit_ns, never hangs, and leaves the context usable: this is the
  * mechanism every pipeline wait of the library uses to turn a stall into
  * RAG_ERR_TIMEOUT. */

@@ -204,8 +204,8 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     const int k = tid;
     const uint32_t lane_off = uint32_t(warp * 32) << 16;
     uint32_t t_glob = 0, n_items = 0;
-    // One item with its rows padded to R; returns false when a wait gave up.
-    auto run_item = [&](auto Rc, int n) -> bool {
+    // One item with its rows padded to R.
+    auto run_item = [&](auto Rc, int n) -> Run {
       constexpr int R = decltype(Rc)::value;
       constexpr int NO = (3 * R + 7) / 8 * 8;   // O^T columns in use, to the next 8
       const int rows = it.n_q * G;
@@ -216,21 +216,21 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
       for (int j = 0; j < NO; ++j) ov[j] = 0u;
       {
-        if (!mbar_wait(&ctl->q_full[n_items & 1], (n_items >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait(&ctl->q_full[n_items & 1], (n_items >> 1) & 1, abort_flag)) return Run::kGaveUp;
         const float* sq = ctl->sq[n_items & 1];
         const int first = p.causal ? it.n_doc - it.n_q : it.n_doc;   // row r sees positions <= first + r / G
         for (int i = 0; i < n; ++i) {
           const uint32_t t = t_glob + i;
           const uint32_t slot = t % kDescSlots;
           const int bsel = int(t & 1u);
-          if (!mbar_wait(&ctl->desc_full[slot], (t / kDescSlots) & 1, abort_flag)) return false;
+          if (!mbar_wait(&ctl->desc_full[slot], (t / kDescSlots) & 1, abort_flag)) return Run::kGaveUp;
           const TileDesc* td = &ctl->desc[slot];
           const float kf = td->ks[k >> 4], lv = td->lv[k >> 4], iv = td->iv[k >> 4];
           const int pos = td->lstart[k >> 4] + (k & 15);
           const bool kvalid = (k & 15) < int(td->nvalid[k >> 4]);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->desc_empty[slot]);
-          if (!mbar_wait(&ctl->s_full[bsel], (t >> 1) & 1, abort_flag)) return false;
+          if (!mbar_wait(&ctl->s_full[bsel], (t >> 1) & 1, abort_flag)) return Run::kGaveUp;
           tc_fence_after();
           uint32_t u[2 * R];
           tmem_ldn<2 * R>(tmem + lane_off + 32u * bsel, u);
@@ -243,7 +243,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             const float mt = warp_max(y[r]);
             if (lane == 0) ctl->red[bsel][r][warp] = mt;
           }
-          named_bar_sync(1, 128);
+          if (named_bar_leave(1, 128, false)) return Run::kTold;
           float alpha[R];
           bool need = false;
 #pragma unroll
@@ -263,7 +263,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           }
           if (need) {   // the same decision in every key thread (the maxima are shared)
             // O^T must hold PV of the previous tile before it is rescaled
-            if (!mbar_wait(&ctl->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) return false;
+            if (!mbar_wait(&ctl->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) return Run::kGaveUp;
             tc_fence_after();
             tmem_ldn<NO>(tmem + lane_off + kColO, ov);
 #pragma unroll
@@ -275,7 +275,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
             tmem_stn<NO>(tmem + lane_off + kColO, ov);
           }
           // this P^T buffer was last read by the PV of tile t - 2
-          if (t >= 2 && !mbar_wait(&ctl->pv_done[bsel], ((t >> 1) + 1) & 1, abort_flag)) return false;
+          if (t >= 2 && !mbar_wait(&ctl->pv_done[bsel], ((t >> 1) + 1) & 1, abort_flag)) return Run::kGaveUp;
           uint8_t* pb = sP + bsel * kPBytes;
 #pragma unroll
           for (int r = 0; r < R; r += 2) {
@@ -303,7 +303,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->q_empty[n_items & 1]);
         // ---- epilogue: O^T of this item, the row sums over the 128 keys
-        if (!mbar_wait(&ctl->o_full, n_items & 1, abort_flag)) return false;
+        if (!mbar_wait(&ctl->o_full, n_items & 1, abort_flag)) return Run::kGaveUp;
         ++n_items;
         tc_fence_after();
         tmem_ldn<NO>(tmem + lane_off + kColO, ov);
@@ -318,7 +318,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
 #pragma unroll
           for (int r = 0; r < R; ++r) ctl->lsum[r][warp] = ls[r];
         }
-        named_bar_sync(1, 128);
+        if (named_bar_leave(1, 128, false)) return Run::kTold;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const float4 l4 = *reinterpret_cast<const float4*>(ctl->lsum[r]);
@@ -345,18 +345,20 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
           if (d == r) reinterpret_cast<float4*>(dst + kHeadDim / 2)[0] = make_float4(mm[r], l, 0.f, 0.f);
         }
       }
-      return true;
+      return Run::kOn;
     };
     int bad = 0;
-    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+    Run run = Run::kOn;
+    while (run == Run::kOn && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
       const int n = it.n;
       const int R = pad_rows(it.n_q * G);   // at most 16 rows on this path
-      const bool ok = R == 4   ? run_item(std::integral_constant<int, 4>{}, n)
-                      : R == 8 ? run_item(std::integral_constant<int, 8>{}, n)
-                               : run_item(std::integral_constant<int, 16>{}, n);
-      if (!ok) bad = 1;
+      run = R == 4   ? run_item(std::integral_constant<int, 4>{}, n)
+            : R == 8 ? run_item(std::integral_constant<int, 8>{}, n)
+                     : run_item(std::integral_constant<int, 16>{}, n);
     }
+    if (run == Run::kGaveUp) bad = 1;
     if (bad) raise_abort(ctl, p.err);
+    if (run != Run::kTold) named_bar_leave(1, 128, bad);
   } else if (warp == 4) {
     // ------------------------------------------------------------ producer
     uint32_t t_glob = 0, n_k = 0, n_v = 0;   // n_k, n_v: K and V tiles issued

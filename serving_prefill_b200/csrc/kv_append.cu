@@ -638,11 +638,13 @@ __device__ __forceinline__ void row_words(const uint8_t* at, uint32_t* u) {
   u[0] = a.x; u[1] = a.y; u[2] = b.x; u[3] = b.y;
 }
 
-// kPlain: all 16 slots are new and their positions lie inside the table.
+// kPlain: all 16 slots are new and their positions lie inside the table. False:
+// the block's other warp gave up a wait.
 template <bool kIsK, bool kPlain>
-__device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& u, const uint8_t* rows,
+__device__ __forceinline__ bool stream_block(const AppendParams& p, const Unit& u, const uint8_t* rows,
                                              const float4* tab, int h, int warp, int lane, float* big,
                                              float* big_finite, int& err) {
+  bool told = false;
   const int c = lane & 15, sub = (warp & 1) * 8 + (lane >> 4);   // first row
   constexpr int kIts = 4;                                        // rows sub, sub + 2, sub + 4, sub + 6
   const int64_t block = (int64_t(p.layer) * p.num_pages + u.page) * p.num_kv_heads + h;
@@ -707,11 +709,12 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) at[warp] = m;
-    named_bar_sync(1 + (warp >> 1), 64);
+    told = named_bar_leave(1 + (warp >> 1), 64, false);
     return fmaxf(at[warp & ~1], at[warp | 1]);
   };
   if (odd) err |= kDevErrRange;
   amax = shared_max(odd ? INFINITY : amax, big);
+  if (told) return false;                       // no wait lies between this round and the block's others
   const bool any_odd = amax == INFINITY;
   if (any_odd) {                                // rare: the scale follows the finite values
     amax = 0.f;
@@ -760,6 +763,7 @@ __device__ __forceinline__ void stream_block(const AppendParams& p, const Unit& 
     }
   }
   if (lane == 0 && !(warp & 1) && (kPlain || u.s0 == 0 || sc.regrow)) *scale_at = sc.now;
+  return true;
 }
 
 }  // namespace
@@ -842,32 +846,40 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
   }
   uint32_t n = 0;
   int err = 0;
-  for (int i = 0; i < p.units_per_block; ++i) {
+  Run run = Run::kOn;   // the two warps of a page block share a named barrier
+  for (int i = 0; i < p.units_per_block && run == Run::kOn; ++i) {
     const Unit u = ctl->units[i];
     if (u.page < 0) continue;
     for (int y = y0; y < groups; y += p.heads_split, ++n) {
       const int s = n % kStreamStages;
       if (!mbar_wait(&ctl->full[s], (n / kStreamStages) & 1, abort_flag)) {
-        if (lane == 0 && p.err) atomicOr(p.err, kDevErrTimeout);
         ctl->abort = 1;
-        return;
+        err |= kDevErrTimeout;
+        run = Run::kGaveUp;
+        break;
       }
       const int r = 8 * y + (warp >> 1);
       const uint8_t* rows = smem + s * kStageBytes + (warp >> 1) * (kHeadDim * 2);
       const float4* tab = tabs + s * kStageTab;
       float* big = ctl->big[n & 1];
       const bool plain = u.s0 == 0 && u.s1 == kPage && (!p.rope || (u.pos >= 0 && u.pos + kPage <= p.n_pos));
+      bool on = true;
       if (r < H) {
-        if (plain) stream_block<true, true>(p, u, rows, tab, r, warp, lane, big, ctl->big_finite, err);
-        else stream_block<true, false>(p, u, rows, tab, r, warp, lane, big, ctl->big_finite, err);
+        on = plain ? stream_block<true, true>(p, u, rows, tab, r, warp, lane, big, ctl->big_finite, err)
+                   : stream_block<true, false>(p, u, rows, tab, r, warp, lane, big, ctl->big_finite, err);
       } else if (r < 2 * H) {
-        if (plain) stream_block<false, true>(p, u, rows, tab, r - H, warp, lane, big, ctl->big_finite, err);
-        else stream_block<false, false>(p, u, rows, tab, r - H, warp, lane, big, ctl->big_finite, err);
+        on = plain ? stream_block<false, true>(p, u, rows, tab, r - H, warp, lane, big, ctl->big_finite, err)
+                   : stream_block<false, false>(p, u, rows, tab, r - H, warp, lane, big, ctl->big_finite, err);
+      }
+      if (!on) {
+        run = Run::kTold;
+        break;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->empty[s]);
     }
   }
+  if (run != Run::kTold) named_bar_leave(1 + (warp >> 1), 64, run == Run::kGaveUp);
   if (err && p.err) atomicOr(p.err, err);
 }
 

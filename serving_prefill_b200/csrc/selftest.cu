@@ -1,8 +1,10 @@
 // Self-test of the device-side failure detection that every pipeline of the
 // library relies on: a bounded mbarrier wait that gives up, raises the CTA's
 // abort flag and records a timeout in the error word, and a second role of
-// the CTA that leaves its own wait as soon as it sees the flag. Nothing here
-// faults or hangs: both waits end, by the limit or by the flag.
+// the CTA that leaves its own wait as soon as it sees the flag; and four warps
+// that share a named barrier, of which one gives up a wait between two rounds:
+// all four have to leave at the same round. Nothing here faults or hangs: the
+// waits end, by the limit or by the flag, and every warp comes to each round.
 #include <cuda_runtime.h>
 
 #include "rag_prefill.h"
@@ -10,19 +12,32 @@
 
 namespace rag {
 
-__global__ void __launch_bounds__(64, 1) wait_selftest_kernel(int32_t* err, uint64_t limit_ns) {
-  __shared__ uint64_t never[2];   // barriers no thread ever arrives on
-  __shared__ int abort_flag;
+__global__ void __launch_bounds__(192, 1) wait_selftest_kernel(int32_t* err, uint64_t limit_ns) {
+  __shared__ uint64_t never[3];   // barriers no thread ever arrives on
+  __shared__ int abort_flag, left[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&never[0], 1);
     mbar_init(&never[1], 1);
+    mbar_init(&never[2], 1);
     abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
   volatile int* abort = &abort_flag;
-  if (lane == 0) {
+  if (warp >= 2) {
+    // rounds 0 .. 3; warp 4 gives up before round 2
+    constexpr int kRounds = 4, kLast = 2;
+    int none = 0, round = 0;
+    Run run = Run::kOn;
+    for (; round < kRounds; ++round) {
+      if (warp == 4 && round == kLast && !mbar_wait_for(&never[2], 0, &none, limit_ns)) run = Run::kGaveUp;
+      if (run == Run::kOn && named_bar_leave(1, 128, false)) run = Run::kTold;
+      if (run != Run::kOn) break;
+    }
+    if (run != Run::kTold) named_bar_leave(1, 128, run == Run::kGaveUp);
+    if (lane == 0) left[warp - 2] = round;
+  } else if (lane == 0) {
     if (warp == 0) {
       // the short wait runs out: report it and tell the other role
       if (!mbar_wait_for(&never[0], 0, abort, limit_ns)) {
@@ -35,6 +50,7 @@ __global__ void __launch_bounds__(64, 1) wait_selftest_kernel(int32_t* err, uint
     }
   }
   __syncthreads();
+  if (threadIdx.x < 4 && left[threadIdx.x] != 2) atomicOr(err, kDevErrGeometry);
 }
 
 }  // namespace rag
@@ -42,7 +58,7 @@ __global__ void __launch_bounds__(64, 1) wait_selftest_kernel(int32_t* err, uint
 extern "C" RAG_API rag_status rag_selftest_wait_timeout(int32_t* device_err, int64_t limit_ns, void* stream) {
   if (!device_err || limit_ns <= 0 || limit_ns > int64_t(rag::kWaitLimitNs)) return RAG_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = rag::launch_plain(rag::wait_selftest_kernel, dim3(1), dim3(64), 0, s, device_err,
+  const cudaError_t e = rag::launch_plain(rag::wait_selftest_kernel, dim3(1), dim3(192), 0, s, device_err,
                                           uint64_t(limit_ns));
   rag::note_cuda_error(e);
   return e == cudaSuccess ? RAG_OK : RAG_ERR_CUDA;
