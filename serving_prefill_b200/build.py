@@ -21,7 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "librag.so")
 SOURCES = ["rag_api.cu", "attn_fwd.cu", "attn_combine.cu", "decode_fwd.cu", "impact.cu", "topk.cu", "simt_f32.cu", "pool_write.cu", "rag_static.cu", "selftest.cu", "recompute.cu", "kv_decode.cu",
            "kv8_api.cu", "kv_append.cu", "kv8_fwd.cu", "kv8_decode.cu"]
-HEADERS = ["ptx.cuh", "common.cuh", "params.cuh", "host.cuh", "kv8.cuh"]
+HEADERS = ["ptx.cuh", "common.cuh", "params.cuh", "host.cuh", "kv8.cuh", "leave.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

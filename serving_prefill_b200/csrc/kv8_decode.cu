@@ -35,6 +35,7 @@
 #include <type_traits>
 
 #include "kv8.cuh"
+#include "leave.cuh"
 #include "params.cuh"
 
 namespace rag {

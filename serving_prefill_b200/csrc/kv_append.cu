@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "kv8.cuh"
+#include "leave.cuh"
 #include "params.cuh"
 
 namespace rag {

@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include "rag_prefill.h"
+#include "leave.cuh"
 #include "params.cuh"
 
 namespace rag {
