@@ -113,7 +113,7 @@ constexpr double kPieceTiles = 4.0;
 static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
   Kv8Plan pl;
   pl.decode = int64_t(b.max_q) * group <= 16 ? 1 : 0;
-  pl.toks_per_block = pl.decode ? 16 / group : kQTiles * (kBM / group);
+  pl.toks_per_block = pl.decode ? std::max(1, 16 / group) : kQTiles * (kBM / group);   // any group, if no request has queries
   pl.item_rows = pl.decode ? 16 : kFwdRows;
   // two CTAs of the decode kernel share an SM; no more CTAs than the batch's
   // capacities can give work to
