@@ -432,7 +432,8 @@ RAG_API rag_status rag_kv_append(const rag_kv_pool* pool, int32_t layer, const r
  * k_scale, v_scale [num_layers][num_pages][num_kv_heads] fp32
  * value = code * scale of its page and head. rag_kv8_append keeps the scales
  * powers of two, at least 2^-24; the attention takes any positive finite scale
- * (of V: at most 128, since V enters the product with the weights as fp16).
+ * (of V: at most 128, since V enters the product with the weights as fp16; below
+ * 2^-64 a scale counts as 2^-64).
  * The codes 0x7f and 0xff (nan) must not stand in slots that hold tokens. */
 typedef struct {
   void* k;
@@ -483,7 +484,7 @@ RAG_API size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch*
  * o       [total_q][num_q_heads][128] bf16, not overlapping q
  * row_lse optional [total_q][num_q_heads] fp32
  * num_q_heads / num_kv_heads may be any whole number up to 128. sm_scale <= 0
- * selects 1 / sqrt(128).
+ * selects 1 / sqrt(128); a positive one below 2^-32 counts as 2^-32.
  * Precision: Q enters the product as two e4m3 parts per value under a
  * power-of-two scale per row (together at least the 8 bits of a bf16 value down
  * to 2^-14 of the row's largest, 2^-18 of it absolute), K as its codes, with

@@ -20,6 +20,12 @@ constexpr int kScaleExpMin = -24;     // smallest block scale the append writes:
 constexpr int kScaleExpMaxK = 120;    // 448 * 2^120 is past the fp32 range
 constexpr int kScaleExpMaxV = 7;      // 448 * 2^7 = 57,344: V enters its product as fp16
 
+// Least scale the attention computes with: a smaller one of K would make the
+// factor of a row and page 0, and 0 * -inf in a masked place nan; a smaller one
+// of V would make its reciprocal, and the row sum, infinite.
+constexpr float kScaleMin = 0x1p-64f;
+constexpr float kSmScaleMin = 0x1p-32f;   // least softmax scale, for the same reason
+
 // Two fp32 values to two e4m3 codes (lo in the low byte), nearest even,
 // saturated at +-448.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -440,7 +446,7 @@ __device__ __forceinline__ bool kv8_take(Kv8Ring* ring, uint32_t j, Kv8Item& it,
 // scales one, so that no tile waits for a load. (Resolved tile by tile, with
 // ids two tiles and scales one tile ahead, every tile cost a load's latency:
 // 2 us a tile of 80 or of 128 keys alike.) A scale outside (0, inf), or of V
-// above 128, is reported and taken as 1.
+// above 128, is reported and taken as 1; one below kScaleMin counts as that.
 template <int kPagesTile>
 struct Kv8Pages {
   static constexpr int kTiles = 32 / kPagesTile;
@@ -469,8 +475,22 @@ struct Kv8Pages {
     v = __ldg(p.v_scale + at);
   }
   __device__ __forceinline__ void settle(const Kv8Params& p) {
-    if (!(cur_k > 0.f && cur_k < INFINITY)) { atomicOr(p.err, kDevErrRange); cur_k = 1.f; }
-    if (!(cur_v > 0.f && cur_v <= 128.f)) { atomicOr(p.err, kDevErrRange); cur_v = 1.f; }
+    if (!(cur_k >= kScaleMin && cur_k < INFINITY)) {
+      if (cur_k > 0.f && cur_k < 1.f) {
+        cur_k = kScaleMin;
+      } else {
+        atomicOr(p.err, kDevErrRange);
+        cur_k = 1.f;
+      }
+    }
+    if (!(cur_v >= kScaleMin && cur_v <= 128.f)) {
+      if (cur_v > 0.f && cur_v < 1.f) {
+        cur_v = kScaleMin;
+      } else {
+        atomicOr(p.err, kDevErrRange);
+        cur_v = 1.f;
+      }
+    }
   }
   // The first window; the next one's ids are on their way.
   __device__ __forceinline__ void start(const Kv8Params& p, const ReqInfo& r, ChunkCache* cc, bool load_chunks,

@@ -321,7 +321,7 @@ rag_status rag_kv8_attn(const rag_kv8_pool* pool, int32_t layer, const rag_batch
   p.split_tiles = pl.split_tiles;
   p.grid = pl.grid;
   p.causal = causal ? 1 : 0;
-  p.scale_log2 = (sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(float(kHeadDim))) * 1.4426950408889634f;
+  p.scale_log2 = (sm_scale > 0.f ? std::max(sm_scale, kSmScaleMin) : 1.0f / std::sqrt(float(kHeadDim))) * 1.4426950408889634f;
   p.k_scale = pool->k_scale;
   p.v_scale = pool->v_scale;
   p.q = static_cast<const __nv_bfloat16*>(q);
