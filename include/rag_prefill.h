@@ -485,14 +485,26 @@ RAG_API size_t rag_kv8_workspace_size(const rag_kv8_pool* pool, const rag_batch*
  * row_lse optional [total_q][num_q_heads] fp32
  * num_q_heads / num_kv_heads may be any whole number up to 128. sm_scale <= 0
  * selects 1 / sqrt(128); a positive one below 2^-32 counts as 2^-32.
+ * Rows are query tokens x num_q_heads / num_kv_heads; the batch's max_q decides
+ * once for all its requests which of two kernels runs, the one for query blocks
+ * of at most 16 rows (a generation step) or the one for longer blocks. A batch
+ * that mixes a prompt with single tokens takes the latter for all of them: two
+ * calls, one for each kind, are faster.
  * Precision: Q enters the product as two e4m3 parts per value under a
- * power-of-two scale per row (together at least the 8 bits of a bf16 value down
- * to 2^-14 of the row's largest, 2^-18 of it absolute), K as its codes, with
- * fp32 sums; the softmax runs in fp32; the weights enter the second product in
- * at least 11 bits (those below 2^-14 of the row's largest with an error of at
- * most 2^-24 of it), V exactly, with fp32 sums (for a caller's own scale that is
- * no power of two, or below 2^-24, query blocks of more than 16 rows take code *
- * scale rounded to fp16). A nan or an infinity in a query makes that row nan.
+ * power-of-two scale per row, at least 2^-24: exact for values of at least 2^-13
+ * of the row's largest in blocks of at most 16 rows (2^-9 in longer ones), others
+ * within 2^-21 (2^-17) of it, or 2^-38 (2^-34) where that is more. K enters as
+ * its codes, with fp32 sums; the softmax runs in fp32 (scores past about 2^24
+ * have no fraction there, and rows with scores past 2^28 may become nan). The
+ * weights enter the second product in at least 11 bits (those below 2^-14 of the
+ * row's largest with an error of at most 2^-24 of it), with fp32 sums. V enters
+ * it exactly in blocks of at most 16 rows. In longer ones it enters as fp16: exact
+ * for power-of-two scales from 2^-15 on, else code * scale rounded to fp16 (half
+ * a step: 2^-11 of the value, 2^-25 below fp16's normal range), and for a
+ * caller's own scale that fp16 does not hold, with the scale rounded to fp16
+ * first (2^-11 of it, 2^-25 below 2^-14). A row whose keys several blocks share is
+ * merged from partial outputs in fp16 (2^-11 of each, or 2^-25). A nan or an
+ * infinity in a query makes that row nan.
  * The workspace's error word collects page, geometry and timeout errors as
  * rag_fused_prefill_attn's, and RAG_ERR_RANGE for a scale outside the range
  * above (it is taken as 1). */

@@ -9,14 +9,20 @@
 // 128 / G tokens to a tile. The scores come from the codes themselves:
 //   q = s_q (hi + lo), hi and lo e4m3, s_q a power of two per row, split once
 //       by kv8_split_q_kernel: a bf16 value's 8 significant bits are two e4m3
-//       significands, so hi + lo is the value itself unless it lies 2^-14 or
-//       more below the row's largest (then off by at most 2^-18 of that one)
+//       significands, so hi + lo is the value itself from s_q / 4 on, where lo's
+//       last bit is e4m3's smallest step, 2^-9 s_q; that is at least from 2^-9 of
+//       the row's largest on, and smaller values are off by at most 2^-10 s_q,
+//       2^-17 of the largest
 //   S = hi K8 + lo K8: two kind::f8f6f4 products of twice the 16-bit rate, so
 //       they cost what one bf16 product would, K tiles go from TMA to the
 //       tensor core untouched, and no page is converted for the scores
 //   score = S * (s_q * scale of the page): one factor per row and page, folded
 //       into the softmax's multiply-add
-// V enters as fp16 (code * scale, exact for scales that are powers of two):
+// V enters as fp16 (code * scale, exact for power-of-two scales from 2^-15 on;
+// below, fp16's smallest step is coarser than the code's, and the value is off by
+// at most 2^-25; another scale is itself rounded to fp16 first, as rounding the
+// product instead made the conversion the slowest role: 147 us against 133 for
+// the 16 prompts):
 // weights in e4m3 would lose what the softmax kept, and splitting them costs
 // the issue-bound softmax warps more than two converting warps cost.
 //   producer warp : per tile 5 + 5 TMA page boxes of 2 KB (K, V), the scales
