@@ -110,6 +110,12 @@ constexpr int kWholeTiles = 2;
 // 2 gives the same plans as 4.)
 constexpr double kPieceTiles = 4.0;
 
+// The kernel is one choice a batch, by its longest query block: both kernels on
+// one line of work would need a line each. A batch that mixes the kinds is faster
+// as two calls: 63 single tokens over about 12,900 keys and a prompt of 100 over
+// 10,000 take 651 us in one, 329 in two; 15 over 3,900 and 100 over 4,000 84 and
+// 73; 63 over 1,000 and 40 over 1,000 90 and 64; 7 and a prompt of 400 over 10,000
+// each 150 and 140.
 static Kv8Plan plan_kv8(const rag_batch& b, int num_kv_heads, int group, int sms) {
   Kv8Plan pl;
   pl.decode = int64_t(b.max_q) * group <= 16 ? 1 : 0;
@@ -267,9 +273,13 @@ rag_status rag_kv8_append(const rag_kv8_pool* pool, int32_t layer, const rag_app
     }
     return RAG_OK;
   }
-  // a block takes several units once the GPU is filled a few times over (512
-  // sequences of 64 tokens, 8 heads: 71.7 us against 74.8 with one), and with
-  // fewer units than SMs only 8 page blocks of one, so that no warp takes two
+  // a block takes several units once the GPU is filled a few times over: its
+  // start (sequence, page ids) is paid once for them. With 1 / 2 / 4 / 8 at most,
+  // 32 query heads with 8 KV heads: 512 sequences of 64 tokens 185 / 179 / 179 /
+  // 179 us (two is the rule's choice), 1,024 of 64 365 / 351 / 343 / 342 (five),
+  // 4,096 of 1 119 / 99 / 87 / 81 (seven); K and V alone: 4,096 of 16, 8 heads
+  // 215 / 189 / 174 / 174 (eight), 4,096 of 32, 1 head 219 / 190 / 156 / 144. With
+  // fewer units than SMs a block takes 8 page blocks of one, so that no warp takes two
   // (64 tokens of 64 sequences 4.9 us against 5.8, 4 prompts of 256 7.5 against
   // 8.3; but 64 prompts of 16 tokens, 192 units, 9.8 against 8.9)
   p.units_per_block = int(std::max<int64_t>(1, std::min<int64_t>(8, units / (8 * num_sms()))));
