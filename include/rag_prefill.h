@@ -379,7 +379,7 @@ RAG_API rag_status rag_recompute_status(const void* plan, int32_t* counts, void*
  *                         may have none: it is not looked at)
  *   start    [n_seqs]     tokens the sequence holds already
  *   page_off [n_seqs+1]   prefix over sequences of pages; they must hold
- *                         start[s] + new tokens
+ *                         start[s] + new tokens, at most 2^31 - 1
  *   page_ids [total_pages]
  *   pos0     [n_seqs]     optional (NULL: 0): position of the sequence's token 0
  * total_new and total_pages bound the prefixes; rows of k, v, q from

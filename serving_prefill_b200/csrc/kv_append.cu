@@ -75,7 +75,7 @@ __device__ __forceinline__ Seq load_seq(const AppendSeqs& a, int s) {
   q.n_pages = p1 - q.p0;
   q.ok = q.t0 >= 0 && q.n >= 0 && t1 <= a.total_new &&
          (q.n == 0 || (q.start >= 0 && q.p0 >= 0 && q.n_pages >= 0 && p1 <= a.total_pages &&
-                       int64_t(q.start) + q.n <= int64_t(q.n_pages) * kPage));
+                       int64_t(q.start) + q.n <= min(int64_t(q.n_pages) * kPage, int64_t(INT32_MAX))));
   return q;
 }
 

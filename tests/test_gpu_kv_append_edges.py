@@ -1,0 +1,54 @@
+"""Appends at the edges of what the descriptors may say."""
+
+import numpy as np
+import pytest
+import torch
+
+import serving_prefill_b200 as sp
+from test_gpu_kv_append import Case
+
+pytestmark = pytest.mark.gpu
+
+TOP = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_a_sequence_of_two_billion_tokens(kind):
+    """A page table of 2^27 + 2 entries. Tokens up to number 2^31 - 2 are stored
+    (at a position that pos0 brings into the table); a call that would go past
+    2^31 - 1 tokens is reported and stores nothing (token numbers are 32 bits)."""
+    case = Case(kind, [0], [40], seed=1)
+    pages = torch.zeros((1 << 27) + 2, dtype=torch.int32, device="cuda")
+    last = (TOP - 20) // 16
+    pages[last:last + 3] = torch.tensor(case.seqs[0][0], dtype=torch.int32)
+    fn = sp.rag_kv8_append if kind == "e4m3" else sp.rag_kv_append
+
+    def call(start, n):
+        s = sp.Append([0, n], [start], [0, pages.numel()], pages, pos0=[-start])
+        fn(case.pool, 1, s, case.k[:n], case.v[:n], rope=case.rope, q=case.q[:n], q_out=case.q_out[:n],
+           device_err=case.err)
+        torch.cuda.synchronize()
+        return int(case.err.item())
+
+    before = case.state()
+    q0 = case.q_out.clone()
+    for start, n in ((TOP - 10, 20), (TOP, 1), (TOP - 19, 20)):
+        case.err.zero_()
+        assert call(start, n) == 2, (start, n)
+        for a, b in zip(case.state(), before):
+            assert a is None or np.array_equal(a, b)
+        assert not case.q_out[:n].any()
+    case.q_out.copy_(q0)
+    case.err.zero_()
+    assert call(TOP - 20, 20) == 0
+    # the same tokens as a short sequence whose first token has the same slot
+    other = Case(kind, [0], [40], seed=1)
+    slot = (TOP - 20) % 16
+    s = sp.Append([0, 20], [slot], [0, 3], other.seqs[0][0], pos0=[-slot])
+    fn(other.pool, 1, s, other.k[:20], other.v[:20], rope=other.rope, q=other.q[:20], q_out=other.q_out[:20],
+       device_err=other.err)
+    torch.cuda.synchronize()
+    assert int(other.err.item()) == 0
+    for a, b in zip(case.state(), other.state()):
+        assert a is None or np.array_equal(a, b)
+    assert torch.equal(case.q_out, other.q_out)
