@@ -354,9 +354,9 @@ __device__ __forceinline__ Unit unit_of(const AppendParams& p, int u, int lane) 
     return x;
   }
   const int first = q.t0 / kPage + 2 * s;   // above u only if tok_off does not rise from 0
-  if (u < first) {
+  if (u < first || (s == 0 && q.t0 > 0)) {   // rows before the first sequence's
     if (report) atomicOr(p.err, kDevErrGeometry);
-    return x;
+    if (u < first) return x;
   }
   const int a = q.start / kPage + (u - first);     // page of the sequence
   if (q.n == 0 || a < 0 || a > (q.start + q.n - 1) / kPage) return x;

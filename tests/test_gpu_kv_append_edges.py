@@ -52,3 +52,28 @@ def test_a_sequence_of_two_billion_tokens(kind):
     for a, b in zip(case.state(), other.state()):
         assert a is None or np.array_equal(a, b)
     assert torch.equal(case.q_out, other.q_out)
+
+
+@pytest.mark.parametrize("kind,H,total", [("bf16", 2, 30), ("e4m3", 2, 30), ("e4m3", 32, 700)])
+@pytest.mark.parametrize("with_q", [True, False])
+@pytest.mark.parametrize("t0", [1, 5, 15, 16, 20])
+def test_rows_before_the_first_sequences_are_reported(kind, H, total, with_q, t0):
+    """tok_off that does not begin at 0: the rows before it belong to no sequence.
+    They are reported, not stored, and their rows of q_out are zero; the sequence
+    itself is stored. (700 tokens of 32 heads take the streamed kernel.)"""
+    case = Case(kind, [0], [total], H=H, G=1, seed=2)
+    fn = sp.rag_kv8_append if kind == "e4m3" else sp.rag_kv_append
+    pages = case.seqs[0][0]
+    q = dict(q=case.q, q_out=case.q_out) if with_q else {}
+    s = sp.Append([t0, total], [0], [0, len(pages)], pages, total_new=total)
+    fn(case.pool, 1, s, case.k, case.v, rope=case.rope, device_err=case.err, **q)
+    torch.cuda.synchronize()
+    assert int(case.err.item()) == 2
+    if with_q:
+        assert not case.q_out[:t0].any() and case.q_out[t0:].any(-1).all()
+    other = Case(kind, [0], [total], H=H, G=1, seed=2)
+    s = sp.Append([0, total - t0], [0], [0, len(pages)], pages)
+    fn(other.pool, 1, s, other.k[t0:], other.v[t0:], rope=other.rope)
+    torch.cuda.synchronize()
+    for a, b in zip(case.state(), other.state()):
+        assert a is None or np.array_equal(a, b)
