@@ -429,15 +429,13 @@ __device__ __forceinline__ bool kv8_put(Kv8Ring* ring, uint32_t j, const Kv8Item
   __syncwarp();
   return true;
 }
-// A reading warp (kWarp), or a reading thread, takes the j-th item. False: the
-// end, or a wait gave up (bad = 1).
-template <bool kWarp>
+// A reading warp takes the j-th item. False: the end, or a wait gave up (bad = 1).
 __device__ __forceinline__ bool kv8_take(Kv8Ring* ring, uint32_t j, Kv8Item& it, volatile int* abort, int& bad) {
   const int s = j % kItemSlots;
   if (!mbar_wait(&ring->full[s], (j / kItemSlots) & 1, abort)) { bad = 1; return false; }
   it = ring->item[s];
-  if (kWarp) __syncwarp();   // every lane has the item before the slot is given back
-  if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&ring->empty[s]);
+  __syncwarp();   // every lane has the item before the slot is given back
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&ring->empty[s]);
   return it.n > 0;
 }
 

@@ -350,7 +350,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     };
     int bad = 0;
     Run run = Run::kOn;
-    while (run == Run::kOn && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+    while (run == Run::kOn && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
       const int n = it.n;
       const int R = pad_rows(it.n_q * G);   // at most 16 rows on this path
       run = R == 4   ? run_item(std::integral_constant<int, 4>{}, n)
@@ -440,7 +440,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     // ------------------------------------------------------------ V slots without a token -> 0
     uint32_t t_glob = 0;
     int bad = 0;
-    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+    while (!bad && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
       const int n = it.n;
       for (int i = 0; i < n; ++i) {
         const uint32_t t = t_glob + i;
@@ -468,7 +468,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
     uint32_t q_iter = 0;
     int bad = 0;
     pdl_wait();               // q may be the previous kernel's output
-    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+    while (!bad && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
       const int rows = it.n_q * G, R = pad_rows(rows);
       const int buf = int(q_iter & 1u);
       if (q_iter >= 2 && !mbar_wait(&ctl->q_empty[buf], ((q_iter >> 1) - 1) & 1, abort_flag)) { bad = 1; break; }
@@ -537,7 +537,7 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       const uint32_t q_lo0 = sdesc_lo(smem_u32(sQ), 16), p_lo0 = sdesc_lo(smem_u32(sP), 16);
       uint32_t t_glob = 0, n_items = 0;
       int bad = 0;
-      while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      while (!bad && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
         const int n = it.n;
         const int R = pad_rows(it.n_q * G);
         const uint32_t idesc_qk = idesc_e4m3_f32(kBN, uint32_t(n_qk(R)), 0, 0);

@@ -225,7 +225,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint32_t n_of = 0;     // items whose O_qt has been read
     int bad = 0;
     pdl_wait();            // the row scales come from the kernel before this one
-    while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+    while (!bad && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
       const int n = it.n;
       const int tok0 = it.rb * p.toks_per_block;
       const bool active = qt == 0 || it.n_q - tok0 > TT;   // Q tile 1 may hold no row
@@ -504,7 +504,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
       const int c = lane & 7;                         // 16 codes: columns 16c .. 16c + 15
       uint32_t t_glob = 0, q_iter = 0;
       int bad = 0;
-      while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+      while (!bad && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
         const int n = it.n;
         if (warp == 10) {
           if (q_iter > 0 && !mbar_wait(&ctl->q_empty, (q_iter - 1) & 1, abort_flag)) { bad = 1; break; }
@@ -579,7 +579,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         uint32_t n_s[kQTiles] = {0, 0};      // tiles done, per Q tile
         uint32_t n_item[kQTiles] = {0, 0};   // items begun, per Q tile
         int bad = 0;
-        while (!bad && kv8_take<true>(&ctl->ring, n_it++, it, abort_flag, bad)) {
+        while (!bad && kv8_take(&ctl->ring, n_it++, it, abort_flag, bad)) {
           const int n = it.n;
           const int n_qt = it.n_q - it.rb * p.toks_per_block > TT ? 2 : 1;
           if (!mbar_wait(&ctl->q_full, q_iter & 1, abort_flag)) { bad = 1; break; }
