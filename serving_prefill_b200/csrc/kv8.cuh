@@ -56,6 +56,53 @@ __device__ __forceinline__ int scale_exp(float amax, int top) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
+// A query row as two e4m3 parts under a power of two s, the smallest with |q| <=
+// 448 s: hi = e4m3(q / s), lo = e4m3(lo_factor (q / s - hi)). Eight lanes a row
+// (whole warp; lanes 8 r .. 8 r + 7), 16 bf16 values each.
+struct QuerySplit {
+  uint4 hi, lo;
+  float scale;   // s; nan where the row holds inf or nan, as the product itself would be (inf - inf)
+
+  __device__ __forceinline__ void split(const uint4& a, const uint4& b, int lane, float lo_factor) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float x[16];
+    float amax = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float m = fabsf(x[j]);
+      odd = odd || !(m < INFINITY);
+      amax = fmaxf(amax, m);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const unsigned votes = __ballot_sync(0xffffffffu, odd);
+    odd = (votes >> (lane & 24)) & 0xffu;
+    const int e = scale_exp(amax, kScaleExpMaxK);
+    const float inv = pow2f(-e);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = x[4 * k + j] * inv;
+      h[k] = e4m3x4(y[0], y[1], y[2], y[3]);
+      const float2 h0 = f16x2_to_f32x2(e4m3x2_to_f16x2(h[k] & 0xffffu));
+      const float2 h1 = f16x2_to_f32x2(e4m3x2_to_f16x2(h[k] >> 16));
+      l[k] = e4m3x4((y[0] - h0.x) * lo_factor, (y[1] - h0.y) * lo_factor, (y[2] - h1.x) * lo_factor,
+                    (y[3] - h1.y) * lo_factor);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+    scale = odd ? __int_as_float(0x7fffffff) : pow2f(e);
+  }
+};
+
 // Tokens appended by one call: sequence s takes rows [tok_off[s], tok_off[s+1])
 // of k, v and q as its tokens start[s], start[s] + 1, ...
 struct AppendSeqs {
@@ -152,6 +199,20 @@ __device__ __forceinline__ void tc_commit_by(uint32_t leader, uint64_t* bar) {
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn_major,
                                                       uint32_t b_mn_major) {
   return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// A role whose wait gave up tells the others of its CTA.
+template <typename Ctrl>
+__device__ __forceinline__ void raise_abort(Ctrl* c, int32_t* err) {
+  if (!c->abort) {
+    atomicOr(err, kDevErrTimeout);
+    c->abort = 1;
+  }
+}
+// Wait bounded by time only (teardown after an abort).
+__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
+  int zero = 0;
+  mbar_wait(bar, parity, &zero);
 }
 
 constexpr int kTile8 = kBN * kHeadDim;       // a K or V tile of codes of the decode kernel: 128 rows of 128 B

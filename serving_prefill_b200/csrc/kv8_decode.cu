@@ -83,17 +83,6 @@ static_assert(offsetof(Ctrl, vnv) % 8 == 0 && offsetof(Ctrl, red) % 16 == 0 && o
 
 constexpr size_t kSmemData = size_t(2) * kQBytes + 2 * kPBytes + size_t(kKSt + kVSt) * kTile8;
 
-__device__ __forceinline__ void raise_abort(Ctrl* c, int32_t* err) {
-  if (!c->abort) {
-    atomicOr(err, kDevErrTimeout);
-    c->abort = 1;
-  }
-}
-__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
-  int zero = 0;
-  mbar_wait(bar, parity, &zero);
-}
-
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -475,52 +464,18 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       uint8_t* dst = sQ + buf * kQBytes;
       for (int r0 = 0; r0 < R; r0 += 4) {
         const int r = r0 + (lane >> 3);
-        float x[16];
-        float amax = 0.f;
-        bool odd = false;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = 0.f;
+        uint4 v[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
         if (r < rows) {
           const uint4* src = reinterpret_cast<const uint4*>(
               p.q + ((int64_t(it.q0) + r / G) * p.num_q_heads + it.g * G + r % G) * kHeadDim + 16 * c);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 v = src[h];
-            const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[8 * h + 2 * j] = __uint_as_float(vw[j] << 16);
-              x[8 * h + 2 * j + 1] = __uint_as_float(vw[j] & 0xffff0000u);
-            }
-          }
+          v[0] = src[0];
+          v[1] = src[1];
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float a = fabsf(x[j]);
-          odd = odd || !(a < INFINITY);
-          amax = fmaxf(amax, a);
-        }
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const unsigned votes = __ballot_sync(0xffffffffu, odd);
-        odd = (votes >> (lane & 24)) & 0xffu;
-        const int e = scale_exp(amax, kScaleExpMaxK);
-        const float inv = pow2f(-e);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-          float y[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = x[4 * k4 + j] * inv;
-          hi[k4] = e4m3x4(y[0], y[1], y[2], y[3]);
-          const float2 h0 = f16x2_to_f32x2(e4m3x2_to_f16x2(hi[k4] & 0xffffu));
-          const float2 h1 = f16x2_to_f32x2(e4m3x2_to_f16x2(hi[k4] >> 16));
-          lo[k4] = e4m3x4((y[0] - h0.x) * 16.f, (y[1] - h0.y) * 16.f, (y[2] - h1.x) * 16.f, (y[3] - h1.y) * 16.f);
-        }
-        *reinterpret_cast<uint4*>(dst + swz(r, 16 * c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(dst + swz(R + r, 16 * c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        // inf and nan make the whole row nan, as in the product itself (inf - inf)
-        if (c == 0) ctl->sq[buf][r] = odd ? __int_as_float(0x7fffffff) : pow2f(e) * p.scale_log2;
+        QuerySplit q;
+        q.split(v[0], v[1], lane, 16.f);
+        *reinterpret_cast<uint4*>(dst + swz(r, 16 * c)) = q.hi;
+        *reinterpret_cast<uint4*>(dst + swz(R + r, 16 * c)) = q.lo;
+        if (c == 0) ctl->sq[buf][r] = q.scale * p.scale_log2;
       }
       fence_proxy_async_smem();
       __syncwarp();

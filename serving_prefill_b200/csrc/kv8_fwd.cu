@@ -113,18 +113,6 @@ constexpr size_t smem_bytes(int num_requests) {
 }
 static_assert(smem_bytes(kMaxRequests) <= 227 * 1024, "shared memory of a CTA");
 
-__device__ __forceinline__ void raise_abort(Ctrl* c, int32_t* err) {
-  if (!c->abort) {
-    atomicOr(err, kDevErrTimeout);
-    c->abort = 1;
-  }
-}
-// Wait bounded by time only (teardown after an abort).
-__device__ __forceinline__ void wait_quiet(uint64_t* bar, uint32_t parity) {
-  int zero = 0;
-  mbar_wait(bar, parity, &zero);
-}
-
 // 32 lanes x 16 columns of 32-bit: thread i of the warp gets lane (base + i).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -673,50 +661,14 @@ __global__ void __launch_bounds__(256) kv8_split_q_kernel(const Kv8Params p, int
   const int c = threadIdx.x & 7;
   const int64_t at = row < rows ? row : rows - 1;
   const uint4* src = reinterpret_cast<const uint4*>(p.q + at * kHeadDim + 16 * c);
-  float x[16];
-  float amax = 0.f;
-  bool odd = false;
   pdl_wait();   // q may be the previous kernel's output, and its attention may still read the split queries
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint4 u = src[k];
-    const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * k + 2 * j] = __uint_as_float(uw[j] << 16);
-      x[8 * k + 2 * j + 1] = __uint_as_float(uw[j] & 0xffff0000u);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float a = fabsf(x[j]);
-    odd = odd || !(a < INFINITY);
-    amax = fmaxf(amax, a);
-  }
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const unsigned votes = __ballot_sync(0xffffffffu, odd);
-  odd = (votes >> (threadIdx.x & 24)) & 0xffu;
-  const int e = scale_exp(amax, kScaleExpMaxK);
-  const float inv = pow2f(-e);
-  uint32_t hi[4], lo[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float y[4], d[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = x[4 * k + j] * inv;
-    hi[k] = e4m3x4(y[0], y[1], y[2], y[3]);
-    const float2 h0 = f16x2_to_f32x2(e4m3x2_to_f16x2(hi[k] & 0xffffu));
-    const float2 h1 = f16x2_to_f32x2(e4m3x2_to_f16x2(hi[k] >> 16));
-    d[0] = y[0] - h0.x; d[1] = y[1] - h0.y; d[2] = y[2] - h1.x; d[3] = y[3] - h1.y;
-    lo[k] = e4m3x4(d[0], d[1], d[2], d[3]);
-  }
+  QuerySplit q;
+  q.split(src[0], src[1], threadIdx.x & 31, 1.f);
   if (row >= rows) return;
   uint8_t* dst = p.qs + row * (2 * kHeadDim) + 16 * c;
-  *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(dst + kHeadDim) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  // inf and nan make the whole row nan, as in the product itself (inf - inf)
-  if (c == 0) p.qscale[row] = odd ? __int_as_float(0x7fffffff) : pow2f(e);
+  *reinterpret_cast<uint4*>(dst) = q.hi;
+  *reinterpret_cast<uint4*>(dst + kHeadDim) = q.lo;
+  if (c == 0) p.qscale[row] = q.scale;
 }
 
 // Merge the partial rows (O, m, l) of every cut unit:
