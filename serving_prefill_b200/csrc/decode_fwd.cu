@@ -24,6 +24,7 @@
 
 #include <type_traits>
 
+#include "leave.cuh"
 #include "params.cuh"
 
 namespace rag {
@@ -256,10 +257,9 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int k = tid;
     const uint32_t lane_off = uint32_t(warp * 32) << 16;
     uint32_t t_glob = 0, n_items = 0;
-    int bad = 0;
     // One item with the rows padded to R (4, 8 or 16: the item's rows are
-    // n_q * G <= 16); returns false when a wait gave up.
-    auto run_item = [&](auto Rc, const Item& it, int w, int n) -> bool {
+    // n_q * G <= 16).
+    auto run_item = [&](auto Rc, const Item& it, int w, int n) -> Run {
       constexpr int R = decltype(Rc)::value;
       const int rows = it.req.n_q * G;
       float m_ref[R], ls[R];
@@ -269,13 +269,13 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t t = t_glob + i;
         const uint32_t slot = t % kDescSlots;
         const int bsel = int(t & 1u);
-        if (!mbar_wait(&ctl->desc_full[slot], (t / kDescSlots) & 1, abort_flag)) return false;
+        if (!mbar_wait(&ctl->desc_full[slot], (t / kDescSlots) & 1, abort_flag)) return Run::kGaveUp;
         const int kind = ctl->desc[slot].kind;
         const int kbase = ctl->desc[slot].kbase;
         const int nv = ctl->desc[slot].nvalid[k >> 4];
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->desc_empty[slot]);
-        if (!mbar_wait(&ctl->s_full[bsel], (t >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait(&ctl->s_full[bsel], (t >> 1) & 1, abort_flag)) return Run::kGaveUp;
         tc_fence_after();
         uint32_t u[kRows];
         tmem_ld16(tmem + lane_off + kColS + 16u * bsel, u);
@@ -307,7 +307,7 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
           for (int r = 0; r < R; ++r) ctl->red[bsel][warp][r] = mt[r];
         }
-        named_bar_sync(1, 128);
+        if (named_bar_leave(1, 128, false)) return Run::kTold;
         float alpha[R];
         bool need = false;
 #pragma unroll
@@ -327,7 +327,7 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         if (need) {   // the same decision in every key thread (the maxima are shared)
           // O^T must hold PV of the previous tile before it is rescaled
-          if (!mbar_wait(&ctl->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) return false;
+          if (!mbar_wait(&ctl->pv_done[(t - 1) & 1], ((t - 1) >> 1) & 1, abort_flag)) return Run::kGaveUp;
           tc_fence_after();
           uint32_t ov[kRows];
           tmem_ld16(tmem + lane_off + kColO, ov);
@@ -347,7 +347,7 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         // this P^T buffer was last read by the PV of tile t - 2; rows past R
         // are left as they are: an output column reads only its own P^T row
-        if (t >= 2 && !mbar_wait(&ctl->pv_done[bsel], ((t >> 1) + 1) & 1, abort_flag)) return false;
+        if (t >= 2 && !mbar_wait(&ctl->pv_done[bsel], ((t >> 1) + 1) & 1, abort_flag)) return Run::kGaveUp;
         uint8_t* pb = sP + bsel * kPBytes;
 #pragma unroll
         for (int r = 0; r < R; ++r) *reinterpret_cast<__half*>(pb + p_offset(r, k)) = __float2half_rn(pr[r]);
@@ -357,7 +357,7 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
       }
       t_glob += n;
       // ---- epilogue: O^T of this item, the row sums over the 128 keys
-      if (!mbar_wait(&ctl->o_full, n_items & 1, abort_flag)) return false;
+      if (!mbar_wait(&ctl->o_full, n_items & 1, abort_flag)) return Run::kGaveUp;
       ++n_items;
       tc_fence_after();
       uint32_t ov[kRows];
@@ -374,7 +374,7 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
         for (int r = 0; r < R; ++r) ctl->lsum[warp][r] = ls[r];
       }
-      named_bar_sync(1, 128);
+      if (named_bar_leave(1, 128, false)) return Run::kTold;
       pdl_wait();   // outputs and partials may still be read by the previous kernel
       const int d = k;   // this thread's TMEM lane of O^T is column d of the output rows
 #pragma unroll
@@ -400,19 +400,20 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
           if (d == r) reinterpret_cast<float4*>(dst + kHeadDim / 2)[0] = make_float4(m_ref[r], l, 0.f, 0.f);
         }
       }
-      return true;
+      return Run::kOn;
     };
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
+    Run run = Run::kOn;
+    for (int w = blockIdx.x; w < total_items && run == Run::kOn; w += gridDim.x) {
       const Item it = decode_item(p, prefix, w);
       const int n = it.t_end - it.t_begin;
       if (n == 0) continue;
       const int rows = it.req.n_q * G;   // <= 16 on this path
-      const bool ok = rows <= 4   ? run_item(std::integral_constant<int, 4>{}, it, w, n)
-                      : rows <= 8 ? run_item(std::integral_constant<int, 8>{}, it, w, n)
-                                  : run_item(std::integral_constant<int, 16>{}, it, w, n);
-      if (!ok) bad = 1;
+      run = rows <= 4   ? run_item(std::integral_constant<int, 4>{}, it, w, n)
+            : rows <= 8 ? run_item(std::integral_constant<int, 8>{}, it, w, n)
+                        : run_item(std::integral_constant<int, 16>{}, it, w, n);
     }
-    if (bad) raise_abort(ctl, p.err);
+    if (run == Run::kGaveUp) raise_abort(ctl, p.err);
+    if (run != Run::kTold) named_bar_leave(1, 128, run == Run::kGaveUp);
   } else if (warp == 4 || warp == 5) {
     // ------------------------------------------------------------ producers
     const bool is_k = (warp == 4);
