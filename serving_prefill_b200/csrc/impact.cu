@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "leave.cuh"
 #include "params.cuh"
 
 namespace rag {
@@ -194,16 +195,19 @@ impact_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int k = (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     uint32_t t_glob = 0;
-    int bad = 0;
     // The row statistics, and the zeroed impact vector, come from the kernels
     // before this one; the producer and MMA warps only read inputs and start
     // on the first tiles while those finish.
     pdl_wait();
-    for (int w = blockIdx.x; w < total_items && !bad; w += gridDim.x) {
+    Run run = Run::kOn;   // the epilogue warps share a named barrier
+    for (int w = blockIdx.x; w < total_items && run == Run::kOn; w += gridDim.x) {
       const ImpItem it = decode_imp_item(p, prefix, w);
       const int n = it.t_end - it.t_begin;
       if (n == 0) continue;
-      named_bar_sync(1, kImpEpiThreads);
+      if (named_bar_leave(1, kImpEpiThreads, false)) {
+        run = Run::kTold;
+        break;
+      }
       if (tid < kImpactRows) {
         const int r = tid;   // one row each
         // per row: -m + log2(1 / (l * H_q)), so that 2^(s*c + bias) is the
@@ -225,7 +229,7 @@ impact_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const uint32_t t = t_glob + i;
         const uint32_t buf = t & 1;
         const uint32_t slot = t % kIDescSlots;
-        if (!mbar_wait(&ctl->desc_full[slot], (t / kIDescSlots) & 1, abort_flag)) { bad = 1; break; }
+        if (!mbar_wait(&ctl->desc_full[slot], (t / kIDescSlots) & 1, abort_flag)) { run = Run::kGaveUp; break; }
         const ImpDesc* d = &ctl->desc[slot];
         const int kind = d->kind;
         bool valid;
@@ -242,7 +246,7 @@ impact_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->desc_empty[slot]);
-        if (!mbar_wait(&ctl->s_full[buf], (t >> 1) & 1, abort_flag)) { bad = 1; break; }
+        if (!mbar_wait(&ctl->s_full[buf], (t >> 1) & 1, abort_flag)) { run = Run::kGaveUp; break; }
         tc_fence_after();
         const uint32_t col = tmem + lane_off + (buf ? 256u : 0u) + c0;
         // 32-column chunks with the next chunk's TMEM load in flight while the
@@ -308,7 +312,8 @@ impact_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       }
       t_glob += n;
     }
-    if (bad) imp_abort(ctl, p.err);
+    if (run == Run::kGaveUp) imp_abort(ctl, p.err);
+    if (run != Run::kTold) named_bar_leave(1, kImpEpiThreads, run == Run::kGaveUp);
   } else if (warp == kWarpProducer) {
     // ------------------------------------------------------------ producer
     uint32_t t_glob = 0, q_iter = 0;
