@@ -385,7 +385,7 @@ RAG_API rag_status rag_recompute_status(const void* plan, int32_t* counts, void*
  * total_new and total_pages bound the prefixes; rows of k, v, q from
  * tok_off[n_seqs] to total_new-1 are padding: not used, and their rows of q_out
  * are left as they were. A page that receives tokens belongs to one sequence of
- * the call. With fixed arrays whose contents the caller advances on the device,
+ * the call, at one place of its list. With fixed arrays whose contents the caller advances on the device,
  * a captured call can be replayed. */
 typedef struct {
   int32_t n_seqs;      /* 0 .. 65536 */

@@ -294,7 +294,8 @@ def new_workspace(pool, batch: Batch, num_q_heads: int, device="cuda", stream=No
     """Workspace for rag_fused_prefill_attn (a KVPool) or rag_kv8_attn (a KV8Pool)."""
     size = rag_kv8_workspace_size if isinstance(pool, KV8Pool) else rag_workspace_size
     n = size(pool, batch, num_q_heads)
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):   # its memory may still be in use on another one
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
     _check(lib().rag_workspace_init(_ptr(ws), n, _stream(stream)), "rag_workspace_init")
     return ws
 
@@ -370,8 +371,10 @@ def _on(dev: int, stream) -> int:
 
 
 def rag_rope_cos_sin(base: float, head_dim: int, n_pos: int, device="cuda", stream=None) -> torch.Tensor:
-    """Table of rotations [n_pos][head_dim / 2][2] = (cos, sin) of p * base^(-2j/head_dim)."""
-    table = torch.empty(max(n_pos, 1), max(head_dim, 2) // 2, 2, device=device)
+    """Table of rotations [n_pos][head_dim / 2][2] = (cos, sin) of p * base^(-2j/head_dim).
+    Allocated, like everything torch makes, for the stream that writes it."""
+    with torch.cuda.stream(stream):
+        table = torch.empty(max(n_pos, 1), max(head_dim, 2) // 2, 2, device=device)
     _check(lib().rag_rope_cos_sin(base, head_dim, n_pos, _ptr(table), _on(table.get_device(), stream)),
            "rag_rope_cos_sin")
     return table[:n_pos]

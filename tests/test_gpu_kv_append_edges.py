@@ -77,3 +77,30 @@ def test_rows_before_the_first_sequences_are_reported(kind, H, total, with_q, t0
     torch.cuda.synchronize()
     for a, b in zip(case.state(), other.state()):
         assert a is None or np.array_equal(a, b)
+
+
+def test_what_the_binding_allocates_belongs_to_the_stream_that_writes_it():
+    """The current stream still has a write to a freed block ahead of it; a table
+    (and a workspace) made on another stream must not take that block."""
+    n_pos = 1 << 16
+    want = sp.rag_rope_cos_sin(10000.0, 128, n_pos)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    pool = sp.KVPool(1, 4, 2, 128)
+    b = sp.Batch([0, 1], [0, 40], [0, 3], [0, 1, 2], [0, 4])
+    size = sp.rag_workspace_size(pool, b, 8)
+    torch.cuda.empty_cache()
+    for make, nbytes in ((lambda: sp.rag_rope_cos_sin(10000.0, 128, n_pos, stream=side), want.nbytes),
+                         (lambda: sp.new_workspace(pool, b, 8, stream=side), size)):
+        block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(200_000_000)                       # about 0.1 s
+        block.fill_(0x55)
+        at = block.data_ptr()
+        del block
+        made = make()
+        assert made.data_ptr() != at
+        torch.cuda.synchronize()
+        if made.dtype == torch.float32:
+            assert torch.equal(made, want)
+        else:
+            assert not made[:4].any()                        # the error word
