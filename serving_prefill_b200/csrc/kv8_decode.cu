@@ -18,11 +18,11 @@
 // bandwidth and a warpgroup, and the kernel is there to stream HBM. Two CTAs
 // share an SM, so that one's item start, tile hand-offs and epilogue run under
 // the other's loads.
-// Measured: 64 requests of about 12,900 keys (1.65 GB) 295 us, 0.85 of the
+// Measured: 64 requests of about 12,900 keys (1.65 GB) 296 us, 0.85 of the
 // measured HBM rate; 16 requests of about 3,900 keys (130 MB) 35 us, of which
 // 5 to 6 us pass before the first K box is issued (loads that follow one
 // another, and code that runs cold), 1.6 more until the first scores and 3 in
-// the combine; one request of 560 keys 8.2 us.
+// the combine; one request of 560 keys 8.3 us.
 // Warps: 0-3 keys, 4 producer (page table -> TMA boxes of 2 KB, scales a tile
 // ahead), 5 MMA, 6 zeroes V slots that hold no token (0 * nan), 7 splits Q one
 // item ahead. Every wait is bounded.

@@ -40,7 +40,7 @@
 // (128 / 80 keys): 506 / 530 us for 256 tokens of 64 heads over 65,792 keys,
 // 156 / 148 us for 16 prompts over ragged chunks, 41.3 / 41.8 us for 100 tokens
 // over 10,100 keys. 80 is kept: the ragged case is the usual one, and the
-// softmax warps hardly spill. (With later steps the 80-key form takes 510, 133
+// softmax warps hardly spill. (With later steps the 80-key form takes 507, 133
 // and 41 us.)
 // What bounds it: a tile of two Q tiles takes 2,700 cycles, of which the tensor
 // core is busy 1,450 (QK at N = 80 is bound by shared-memory reads of its
