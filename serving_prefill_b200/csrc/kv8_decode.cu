@@ -419,8 +419,10 @@ kv8_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
       if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
     }
     if (bad) raise_abort(ctl, p.err);
-    // let every copy this warp issued land before the CTA exits
-    if (lane == 0 && ctl->abort) {
+    // Let every copy this warp issued land before the CTA exits, whether a role
+    // has given up by now or does so later. (They have landed, or the others
+    // still wait for them: it costs nothing.)
+    if (lane == 0) {
       for (uint32_t t = n_k > kKSt ? n_k - kKSt : 0; t < n_k; ++t) wait_quiet(&ctl->kfull[t % kKSt], (t / kKSt) & 1);
       for (uint32_t t = n_v > kVSt ? n_v - kVSt : 0; t < n_v; ++t) wait_quiet(&ctl->vfull[t % kVSt], (t / kVSt) & 1);
     }

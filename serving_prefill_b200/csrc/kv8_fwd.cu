@@ -475,8 +475,10 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (lane == 0) p.cuts[blockIdx.x] = walk.cut;
       }
       if (bad) raise_abort(ctl, p.err);
-      // let every copy this warp issued land before the CTA exits
-      if (lane == 0 && ctl->abort) {
+      // Let every copy this warp issued land before the CTA exits, whether a role
+      // has given up by now or does so later. (They have landed, or the others
+      // still wait for them: it costs nothing.)
+      if (lane == 0) {
         for (uint32_t t = n_k > kKSt ? n_k - kKSt : 0; t < n_k; ++t) wait_quiet(&ctl->kfull[t % kKSt], (t / kKSt) & 1);
         for (uint32_t t = n_v > kRSt ? n_v - kRSt : 0; t < n_v; ++t) wait_quiet(&ctl->rfull[t % kRSt], (t / kRSt) & 1);
       }
@@ -553,7 +555,7 @@ kv8_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         t_glob += n;
       }
       if (bad) raise_abort(ctl, p.err);
-      if (lane == 0 && q_iter > 0 && ctl->abort) wait_quiet(&ctl->q_full, (q_iter - 1) & 1);
+      if (lane == 0 && q_iter > 0) wait_quiet(&ctl->q_full, (q_iter - 1) & 1);
       __syncwarp();
     } else {
       // ------------------------------------------------------------ MMA issuer (warp 9)

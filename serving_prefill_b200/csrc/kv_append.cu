@@ -836,8 +836,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv8_append_stream_kernel(co
       if (lane == 0 && p.err) atomicOr(p.err, kDevErrTimeout);
       ctl->abort = 1;
     }
-    // let every copy this warp issued land before the block exits
-    if (lane == 0 && ctl->abort) {
+    // Let every copy this warp issued land before the block exits, whether a
+    // warp has given up by now or does so later. (They have landed, or the others
+    // still wait for them: it costs nothing.)
+    if (lane == 0) {
       int zero = 0;
       for (uint32_t t = n > kStreamStages ? n - kStreamStages : 0; t < n; ++t)
         mbar_wait(&ctl->full[t % kStreamStages], (t / kStreamStages) & 1, &zero);
