@@ -27,17 +27,17 @@ __global__ void __launch_bounds__(192, 1) wait_selftest_kernel(int32_t* err, uin
   __syncthreads();
   volatile int* abort = &abort_flag;
   if (warp >= 2) {
-    // rounds 0 .. 3; warp 4 gives up before round 2
-    constexpr int kRounds = 4, kLast = 2;
-    int none = 0, round = 0;
+    // four times to the barrier; warp 4 gives up before the third
+    constexpr int kTimes = 4, kLast = 2;
+    int none = 0, done = 0;
     Run run = Run::kOn;
-    for (; round < kRounds; ++round) {
-      if (warp == 4 && round == kLast && !mbar_wait_for(&never[2], 0, &none, limit_ns)) run = Run::kGaveUp;
+    for (; done < kTimes; ++done) {
+      if (warp == 4 && done == kLast && !mbar_wait_for(&never[2], 0, &none, limit_ns)) run = Run::kGaveUp;
       if (run == Run::kOn && named_bar_leave(1, 128, false)) run = Run::kTold;
       if (run != Run::kOn) break;
     }
     if (run != Run::kTold) named_bar_leave(1, 128, run == Run::kGaveUp);
-    if (lane == 0) left[warp - 2] = round;
+    if (lane == 0) left[warp - 2] = done;
   } else if (lane == 0) {
     if (warp == 0) {
       // the short wait runs out: report it and tell the other role
